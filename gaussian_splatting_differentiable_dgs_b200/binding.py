@@ -96,6 +96,16 @@ class gs_adam_args(C.Structure):
                 ("eps", C.c_double), ("step", C.c_int32), ("reserved", C.c_int32)]
 
 
+class gs_matrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("row_stride", C.c_int64),
+                ("col_stride", C.c_int64), ("cols", C.c_int32), ("dtype", C.c_int32)]
+
+
+class gs_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("row_stride", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
 SYMBOLS = [
     "gs_version", "gs_status_string", "gs_check", "gs_launch_counter",
     "gs_project_workspace_size", "gs_project",
@@ -111,6 +121,8 @@ SYMBOLS = [
     "gs_raster_fwd", "gs_loss_l1", "gs_loss_total", "gs_ssim_workspace_size", "gs_loss_ssim",
     "gs_raster_bwd",
     "gs_project_bwd", "gs_adam",
+    "gs_lookup", "gs_lookup_bwd_workspace_size", "gs_lookup_plan", "gs_lookup_bwd",
+    "gs_grad_norm_workspace_size", "gs_grad_norm", "gs_grad_clip", "gs_adam_clipped",
 ]
 
 
@@ -165,6 +177,15 @@ def _load():
         "gs_project_bwd": (i32, [P(gs_model), P(gs_camera), P(gs_proj), i64, p, p, i64, p, p,
                                  P(gs_adam_args), p, p]),
         "gs_adam": (i32, [p, p, p, p, i64, p, i64, i64, i32, P(gs_adam_args), p]),
+        "gs_lookup": (i32, [P(gs_matrix), p, i64, p, C.c_double, P(gs_matrix), p, p]),
+        "gs_lookup_bwd_workspace_size": (sz, [i64, i64, i32, i32]),
+        "gs_lookup_plan": (i32, [p, i64, p, i64, i64, i32, p, sz, p, p]),
+        "gs_lookup_bwd": (i32, [P(gs_matrix), p, i64, p, C.c_double, P(gs_matrix), u32, p, sz, p,
+                                p]),
+        "gs_grad_norm_workspace_size": (sz, [i32]),
+        "gs_grad_norm": (i32, [P(gs_tensor), i32, C.c_double, C.c_double, p, p, sz, p, p]),
+        "gs_grad_clip": (i32, [P(gs_tensor), P(gs_tensor), i32, p, p]),
+        "gs_adam_clipped": (i32, [p, p, p, p, i64, p, i64, i64, i32, P(gs_adam_args), p, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -488,3 +509,186 @@ def gs_project_bwd(model: gs_model, cam: gs_camera, proj: gs_proj, n_cand, g2d, 
 def gs_adam(params, m, v, g, g_stride, slot, n, n_pad, P, args: gs_adam_args, stream=None):
     return _ok("gs_adam", _L.gs_adam(ptr(params), ptr(m), ptr(v), ptr(g), g_stride, ptr(slot), n,
                                      n_pad, P, C.byref(args), _stream(stream)))
+
+
+# ---- table lookup and its gradient -----------------------------------------
+
+GS_F32, GS_F16, GS_BF16 = 0, 1, 2
+GS_LOOKUP_ACCUMULATE = 1
+GS_LOOKUP_PLANNED = 2
+
+
+def _dtypes():
+    import torch
+    return {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16}
+
+
+class _OnDevice:
+    """Checks that tensors live on one CUDA device, and makes that device the
+    current one for the call (kernels and the default stream belong to it)."""
+
+    def __init__(self, name, *tensors):
+        import torch
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda or (dev is not None and t.get_device() != dev):
+                raise ValueError(f"{name}: tensors must be on one CUDA device")
+            dev = t.get_device()
+        self.guard = (torch.cuda.device(dev)
+                      if dev is not None and dev != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def matrix(t) -> gs_matrix:
+    """Descriptor of a 2-D tensor: rows behind one another or planes (a
+    transposed view of a planar buffer)."""
+    code = _dtypes().get(t.dtype)
+    if t.dim() != 2 or code is None:
+        raise ValueError("a matrix is a 2-D float32, float16 or bfloat16 tensor, not "
+                         f"{t.dim()}-D {t.dtype}")
+    rows, cols = t.shape
+    rs, cs = t.stride()
+    # the stride of an axis of one element is arbitrary
+    if cols == 1 and not (rs == 1 and cs >= rows):
+        cs = 1
+    elif rows <= 1 and cs == 1:
+        rs = cols
+    elif rows <= 1 and rs != 1:
+        rs = 1
+    return gs_matrix(t.data_ptr(), rows, rs, cs, cols, code)
+
+
+def _ids(name, t):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    return t
+
+
+def _nbytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def gs_lookup(table, ids, out, scale=1.0, index=None, dev_status=None, stream=None):
+    """out[j] = scale * table[ids[j]] (or ids[index[j]]); out is written in the
+    layout its strides say and returned."""
+    _ids("ids", ids), _ids("index", index)
+    if index is not None and index.numel() < out.shape[0]:
+        raise ValueError("index is shorter than out has rows")
+    with _OnDevice("gs_lookup", table, ids, out, index, dev_status):
+        _ok("gs_lookup", _L.gs_lookup(C.byref(matrix(table)), ptr(ids), ids.numel(), ptr(index),
+                                      float(scale), C.byref(matrix(out)), ptr(dev_status),
+                                      _stream(stream)))
+    return out
+
+
+def gs_lookup_bwd_workspace_size(g, rows) -> int:
+    """Workspace of gs_lookup_bwd for a gradient like g ([n][cols]) of a table
+    of `rows` rows."""
+    m = matrix(g)
+    return int(_L.gs_lookup_bwd_workspace_size(m.rows, rows, m.cols, int(m.col_stride != 1)))
+
+
+def gs_lookup_plan(ids, n, rows, cols, ws, index=None, dev_status=None, stream=None):
+    """Sorts n ids into ws for gs_lookup_bwd(..., planned=True)."""
+    _ids("ids", ids), _ids("index", index)
+    if index is not None and index.numel() < n:
+        raise ValueError("index is shorter than n")
+    with _OnDevice("gs_lookup_plan", ids, index, ws, dev_status):
+        return _ok("gs_lookup_plan", _L.gs_lookup_plan(
+            ptr(ids), ids.numel(), ptr(index), n, rows, cols, ptr(ws), _nbytes(ws),
+            ptr(dev_status), _stream(stream)))
+
+
+def gs_lookup_bwd(g, ids, dtable, ws, scale=1.0, index=None, accumulate=False, planned=False,
+                  dev_status=None, stream=None):
+    """dtable[k] (+)= scale * sum of g[j] over the items with id k; returns
+    dtable."""
+    _ids("ids", ids), _ids("index", index)
+    if index is not None and index.numel() < g.shape[0]:
+        raise ValueError("index is shorter than g has rows")
+    flags = (GS_LOOKUP_ACCUMULATE if accumulate else 0) | (GS_LOOKUP_PLANNED if planned else 0)
+    with _OnDevice("gs_lookup_bwd", g, ids, dtable, ws, index, dev_status):
+        _ok("gs_lookup_bwd", _L.gs_lookup_bwd(
+            C.byref(matrix(g)), ptr(ids), ids.numel(), ptr(index), float(scale),
+            C.byref(matrix(dtable)), flags, ptr(ws), _nbytes(ws), ptr(dev_status),
+            _stream(stream)))
+    return dtable
+
+
+# ---- global gradient norm and clipping --------------------------------------
+
+class TensorList:
+    """Descriptors of a list of tensors (kept alive), built once and passed to
+    gs_grad_norm and gs_grad_clip."""
+
+    def __init__(self, tensors):
+        codes = _dtypes()
+        self.tensors = list(tensors)
+        self.count = len(self.tensors)
+        self.array = (gs_tensor * max(self.count, 1))()
+        for k, t in enumerate(self.tensors):
+            code = codes.get(t.dtype)
+            if code is None:
+                raise ValueError(f"tensor {k}: {t.dtype} is not float32, float16 or bfloat16")
+            if t.is_contiguous():
+                rows, cols, rs = 1, t.numel(), t.numel()
+            elif t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+                rows, cols, rs = t.shape[0], t.shape[1], t.stride(0)
+            elif t.dim() == 2 and t.shape[1] == 1 and t.stride(0) >= 1:
+                rows, cols, rs = t.shape[0], 1, t.stride(0)
+            else:
+                raise ValueError(f"tensor {k} is neither contiguous nor rows of contiguous "
+                                 f"elements (shape {tuple(t.shape)}, strides {t.stride()})")
+            self.array[k] = gs_tensor(t.data_ptr(), rows, cols, rs, code, 0)
+
+
+def tensor_list(tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def gs_grad_norm_workspace_size(tensors) -> int:
+    """tensors: a list of tensors, a TensorList or their number."""
+    count = tensors if isinstance(tensors, int) else tensor_list(tensors).count
+    return int(_L.gs_grad_norm_workspace_size(count))
+
+
+def gs_grad_norm(tensors, max_norm, clip, ws, eps=1e-6, dev_status=None, stream=None):
+    """clip[0] = global L2 norm, clip[1] = min(1, max_norm / (norm + eps))."""
+    import torch
+    tl = tensor_list(tensors)
+    if clip.dtype != torch.float32 or clip.numel() < 2 or not clip.is_contiguous():
+        raise ValueError("clip must be a contiguous float32 tensor of 2 values")
+    with _OnDevice("gs_grad_norm", clip, ws, dev_status, *tl.tensors):
+        return _ok("gs_grad_norm", _L.gs_grad_norm(tl.array, tl.count, float(max_norm), float(eps),
+                                                   ptr(clip), ptr(ws), _nbytes(ws),
+                                                   ptr(dev_status), _stream(stream)))
+
+
+def gs_grad_clip(src, dst, clip, stream=None):
+    """dst[i] = clip[1] * src[i] for lists of tensors (dst may be src)."""
+    s, d = tensor_list(src), tensor_list(dst)
+    if s.count != d.count:
+        raise ValueError(f"{s.count} tensors to clip into {d.count}")
+    for x, y in zip(s.tensors, d.tensors):
+        if x.shape != y.shape:
+            raise ValueError(f"shape {tuple(x.shape)} to clip into {tuple(y.shape)}")
+    with _OnDevice("gs_grad_clip", clip, *s.tensors, *d.tensors):
+        return _ok("gs_grad_clip", _L.gs_grad_clip(s.array, d.array, s.count, ptr(clip),
+                                                   _stream(stream)))
+
+
+def gs_adam_clipped(params, m, v, g, g_stride, slot, n, n_pad, P, args: gs_adam_args, clip,
+                    stream=None):
+    return _ok("gs_adam_clipped", _L.gs_adam_clipped(
+        ptr(params), ptr(m), ptr(v), ptr(g), g_stride, ptr(slot), n, n_pad, P, C.byref(args),
+        ptr(clip), _stream(stream)))

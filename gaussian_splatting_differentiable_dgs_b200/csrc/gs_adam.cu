@@ -264,6 +264,23 @@ k_adam(float* __restrict__ P, float* __restrict__ m, float* __restrict__ v,
   }
 }
 
+// Adam on the clipped gradient: g is scaled by the coefficient clip[1] of
+// gs_grad_norm as it is read, so clipping costs no pass of its own.
+__global__ void __launch_bounds__(kThreads)
+k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__ v,
+               const float* __restrict__ g, int64_t g_stride, const int32_t* __restrict__ slot,
+               int64_t n, int64_t n_pad, int nP, const float* __restrict__ clip, AdamK a) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const float c = clip[1];
+  const int64_t col = slot ? slot[i] : i;
+  const bool has = col >= 0 && col < g_stride;
+  for (int plane = 0; plane < nP; ++plane) {
+    const float gg = has ? c * g[(int64_t)plane * g_stride + col] : 0.0f;
+    adam_update(P, m, v, (int64_t)plane * n_pad + i, gg, a);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Fused path, stage 1: geometric gradients of each candidate, i.e.
 // everything except the SH coefficients and the view-direction term of the
@@ -694,6 +711,21 @@ extern "C" gs_status gs_adam(float* params, float* m, float* v, const float* g, 
   if (!slot && g_stride < n) return GS_ERR_ARG;
   k_adam<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, to_stream(stream)>>>(
       params, m, v, g, g_stride, slot, n, n_pad, P, a);
+  GS_LAUNCH_CHECK();
+  return GS_OK;
+}
+
+extern "C" gs_status gs_adam_clipped(float* params, float* m, float* v, const float* g,
+                                     int64_t g_stride, const int32_t* slot, int64_t n,
+                                     int64_t n_pad, int32_t P, const gs_adam_args* args,
+                                     const float* clip, gs_stream stream) {
+  AdamK a;
+  if (!make_adam(args, &a) || n < 0 || n_pad < n || P <= 0) return GS_ERR_ARG;
+  if (n == 0) return GS_OK;
+  if (!params || !m || !v || !g || !clip) return GS_ERR_ARG;
+  if (!slot && g_stride < n) return GS_ERR_ARG;
+  k_adam_clipped<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, to_stream(stream)>>>(
+      params, m, v, g, g_stride, slot, n, n_pad, P, clip, a);
   GS_LAUNCH_CHECK();
   return GS_OK;
 }

@@ -582,6 +582,98 @@ gs_status gs_adam(float* params, float* m, float* v, const float* g,
                   int64_t n_pad, int32_t P, const gs_adam_args* args,
                   gs_stream stream);
 
+/* ---- 10. table lookup and its gradient ------------------------------------
+ * Additions of this library (no counterpart on the pages): parameters shared
+ * by many items, e.g. one colour table for all Gaussians or an embedding per
+ * view.  Element types of these calls: */
+#define GS_F32 0
+#define GS_F16 1
+#define GS_BF16 2
+
+/* A matrix of `rows` x `cols` elements at data[r * row_stride + c *
+ * col_stride] (strides in elements).  One of the strides is 1 and the other
+ * spans at least the contiguous axis: rows behind one another (col_stride 1)
+ * or planes (row_stride 1), the model's layout. */
+typedef struct gs_matrix {
+  void* data;
+  int64_t rows;
+  int64_t row_stride, col_stride;
+  int32_t cols;
+  int32_t dtype;  /* GS_F32, GS_F16 or GS_BF16 */
+} gs_matrix;
+
+/* gs_lookup: out[j][c] = scale * table[id_j][c], rounded once to out's type,
+ * for j < out->rows, with id_j = ids[j], or ids[index[j]] if index is not
+ * NULL (index: out->rows positions in [0, n_ids); without it n_ids must be at
+ * least out->rows).  id_j < 0 gives a row of zeros; an id >= table->rows or an
+ * index out of range gives zeros too and sets GS_DEV_BOUNDS.  The table's
+ * rows are contiguous (col_stride 1, else GS_ERR_UNSUPPORTED); out has either
+ * layout.  Elements of out's buffer outside the matrix stay as they were.
+ * out must not overlap the inputs. */
+gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
+                    const int32_t* index, double scale, const gs_matrix* out,
+                    int32_t* dev_status, gs_stream stream);
+
+/* gs_lookup_bwd: the gradient of gs_lookup's table,
+ *   dtable[k][c] = scale * sum over {j : id_j = k} of g[j][c]
+ * (+= with GS_LOOKUP_ACCUMULATE), fp32, rows contiguous; rows of the table
+ * that no item uses get zero.  Items with id_j < 0 or out of range add
+ * nothing (their g is not read).  The items are sorted by id and summed in
+ * fp32 in a fixed order: equal inputs give equal bits.  At most 2^31 - 1
+ * items and rows.
+ * ws: gs_lookup_bwd_workspace_size(n, rows, cols) bytes, planes: whether g is
+ * in planes (col_stride other than 1).  gs_lookup_plan writes the
+ * sorted order of ids that stay the same for many gradients into ws;
+ * gs_lookup_bwd with GS_LOOKUP_PLANNED and the same ids, index, n, rows, cols
+ * and ws then skips the sort.  The order stays valid until a call without
+ * that flag uses ws. */
+#define GS_LOOKUP_ACCUMULATE 1u
+#define GS_LOOKUP_PLANNED 2u
+size_t gs_lookup_bwd_workspace_size(int64_t n, int64_t rows, int32_t cols,
+                                    int32_t planes);
+gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids,
+                         const int32_t* index, int64_t n, int64_t rows,
+                         int32_t cols, void* ws, size_t ws_bytes,
+                         int32_t* dev_status, gs_stream stream);
+gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64_t n_ids,
+                        const int32_t* index, double scale,
+                        const gs_matrix* dtable, uint32_t flags, void* ws,
+                        size_t ws_bytes, int32_t* dev_status, gs_stream stream);
+
+/* ---- 11. global gradient norm and clipping ---------------------------------
+ * Additions of this library.  A tensor is `rows` pieces of `cols` contiguous
+ * elements, row_stride elements apart (rows = 1: one contiguous piece; the
+ * first n columns of a planar [P][n_pad] gradient: rows = P, cols = n,
+ * row_stride = n_pad).  Tensors with no elements are allowed. */
+typedef struct gs_tensor {
+  void* data;
+  int64_t rows, cols, row_stride;
+  int32_t dtype;  /* GS_F32, GS_F16 or GS_BF16 */
+  int32_t reserved;
+} gs_tensor;
+
+/* gs_grad_norm: clip[0] = N = sqrt(sum of the squares of all elements of all
+ * tensors), clip[1] = c = min(1, max_norm / (N + eps)) (device, 8-byte
+ * aligned; the sum and both values are formed in fp64 in a fixed order).
+ * max_norm and eps must be finite and >= 0.  If N is infinite c = 0, if N is
+ * NaN c is NaN, and GS_DEV_NONFINITE is set in both cases.  The tensors'
+ * descriptors are read on the host during the call.
+ * gs_grad_clip: dst = c * src for every element, rounded once, c = clip[1];
+ * src[i] and dst[i] have the same type and as many elements, in the same rows
+ * and columns unless one of them is a single piece, and are the same memory
+ * (in place) or lie apart (from the first to the last element).
+ * gs_adam_clipped: gs_adam on the gradient c * g. */
+size_t gs_grad_norm_workspace_size(int32_t count);
+gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, double max_norm,
+                       double eps, float* clip, void* ws, size_t ws_bytes,
+                       int32_t* dev_status, gs_stream stream);
+gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst,
+                       int32_t count, const float* clip, gs_stream stream);
+gs_status gs_adam_clipped(float* params, float* m, float* v, const float* g,
+                          int64_t g_stride, const int32_t* slot, int64_t n,
+                          int64_t n_pad, int32_t P, const gs_adam_args* args,
+                          const float* clip, gs_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

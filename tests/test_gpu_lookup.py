@@ -1,0 +1,352 @@
+"""The table lookup and its gradient against plain 64-bit forms.
+
+Tolerances count roundings (u = 2^-24 for fp32): the lookup rounds the product
+once in fp32 and once to the output's type; a sum of m terms in any order
+differs from the exact one by at most (m - 1) u times the sum of the terms'
+sizes, and the scale rounds once more."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import B
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+# half of the smallest subnormal step
+TINY = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+
+
+@pytest.fixture(scope="module")
+def b():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    torch.cuda.set_device(0)
+    return B()
+
+
+def planes(n, cols, dtype, pad=3, fill=0.0):
+    """(buffer, view [n][cols]) of a planar buffer with padding behind each plane."""
+    buf = torch.full((cols, n + pad), fill, dtype=dtype, device="cuda")
+    return buf, buf[:, :n].t()
+
+
+def layout(x, kind):
+    """x [n][cols] on the device as rows, padded rows, offset rows or planes."""
+    n, cols = x.shape
+    if kind == "rows":
+        return x.contiguous()
+    if kind == "padded":
+        buf = torch.zeros((n, cols + 5), dtype=x.dtype, device="cuda")
+        buf[:, :cols] = x
+        return buf[:, :cols]
+    if kind == "offset":  # starts one element past an aligned address
+        buf = torch.zeros(n * cols + 1, dtype=x.dtype, device="cuda")
+        buf[1:] = x.reshape(-1)
+        return buf[1:].view(n, cols)
+    if kind == "planes":
+        return x.t().contiguous().t()
+    buf, view = planes(n, cols, x.dtype)
+    view.copy_(x)
+    return view
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def make_ids(n, rows, seed, holes=0.1, hot=0.0):
+    g = gen(seed)
+    ids = torch.randint(rows, (n,), generator=g, device="cuda", dtype=torch.int32)
+    r = torch.rand(n, generator=g, device="cuda")
+    ids[r < hot] = rows // 3
+    ids[r > 1 - holes] = -1
+    return ids
+
+
+# ---- lookup ------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 2, 31, 33, 257, 1000, 40_001])
+@pytest.mark.parametrize("cols", [1, 3, 4, 12, 27, 48, 130])
+@pytest.mark.parametrize("kind", ["rows", "padded", "offset", "planes", "padded_planes"])
+def test_lookup(b, n, cols, kind):
+    rows = 1 + (n * 7) % 301
+    for k, (tt, to) in enumerate([(torch.float32, torch.float32), (torch.bfloat16, torch.float32),
+                                  (torch.float16, torch.float16), (torch.float32, torch.bfloat16),
+                                  (torch.bfloat16, torch.bfloat16), (torch.float16, torch.bfloat16),
+                                  (torch.float32, torch.float16)]):
+        table = torch.randn(rows, cols, generator=gen(n + k), device="cuda").to(tt)
+        table = layout(table, ("rows", "padded", "offset")[k % 3])
+        ids = make_ids(n, rows, n + cols + k)
+        out = layout(torch.full((n, cols), 7.0, dtype=to, device="cuda"), kind)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        scale = (1.0, 0.75, -3.0)[k % 3]
+        b.gs_lookup(table, ids, out, scale=scale, dev_status=st)
+        ref = torch.where((ids >= 0)[:, None], scale * table.double()[ids.clamp(min=0).long()], 0.0)
+        err = (out.double() - ref).abs()
+        assert (err <= (HALF_STEP[to] + 2 * U) * ref.abs() + TINY[to]).all()
+        assert int(st) == 0
+
+
+@pytest.mark.parametrize("kind", ["padded", "padded_planes"])
+def test_lookup_leaves_the_padding(b, kind):
+    n, cols = 77, 12
+    table = torch.randn(9, cols, generator=gen(1), device="cuda")
+    ids = make_ids(n, 9, 2)
+    if kind == "padded":
+        buf = torch.full((n + 4, cols + 5), 3.0, device="cuda")
+        out = buf[:n, :cols]
+    else:
+        buf = torch.full((cols + 2, n + 5), 3.0, device="cuda")
+        out = buf[:cols, :n].t()
+    b.gs_lookup(table, ids, out)
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    if kind == "padded":
+        keep[:n, :cols] = False
+    else:
+        keep[:cols, :n] = False
+    assert (buf[keep] == 3.0).all()
+
+
+def test_lookup_through_an_index_and_ids_out_of_range(b):
+    n, rows, cols = 500, 40, 27
+    table = torch.randn(rows, cols, generator=gen(3), device="cuda")
+    ids = make_ids(900, rows, 4)
+    index = torch.randint(900, (n,), generator=gen(5), device="cuda", dtype=torch.int32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = b.gs_lookup(table, ids, torch.empty(n, cols, device="cuda"), index=index, dev_status=st)
+    got = ids[index.long()]
+    ref = torch.where((got >= 0)[:, None], table[got.clamp(min=0).long()], 0.0)
+    assert torch.equal(out, ref) and int(st) == 0
+    for bad_ids, bad_index in ((rows, 0), (2 ** 31 - 1, 0), (0, 900), (0, -1), (0, 2 ** 31 - 1)):
+        ids2, index2 = ids.clone(), index.clone()
+        index2[17] = bad_index if bad_index else 3
+        if bad_ids:
+            ids2[3] = bad_ids
+        st.zero_()
+        out = b.gs_lookup(table, ids2, torch.empty(n, cols, device="cuda"), index=index2, dev_status=st)
+        assert (out[17] == 0).all() and int(st) == 2
+        same = (index2 != 3) & (index2 == index)
+        assert torch.equal(out[same], ref[same])
+        assert b.gs_check(st) == b.GS_ERR_BOUNDS and int(st) == 0
+
+
+def test_lookup_keeps_non_finite_values_to_their_rows(b):
+    table = torch.randn(5, 6, generator=gen(6), device="cuda")
+    table[2, 1], table[2, 4] = float("nan"), float("inf")
+    ids = torch.tensor([0, 2, -1, 4, 1], dtype=torch.int32, device="cuda")
+    out = b.gs_lookup(table, ids, torch.empty(5, 6, device="cuda"), scale=2.0)
+    assert torch.isfinite(out[[0, 2, 3, 4]]).all()
+    assert torch.isnan(out[1, 1]) and torch.isinf(out[1, 4])
+
+
+def test_lookup_of_no_rows_launches_nothing(b):
+    n0 = b.gs_launch_counter()
+    out = torch.empty((0, 4), device="cuda")
+    b.gs_lookup(torch.ones(3, 4, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"), out)
+    assert b.gs_launch_counter() == n0
+
+
+def test_lookup_past_32_bit_offsets(b):
+    """Planes and rows whose element offsets pass 2^31."""
+    n, cols, rows = 45_000_001, 48, 7
+    table = torch.randn(rows, cols, generator=gen(7), device="cuda").half()
+    ids = torch.randint(rows, (n,), generator=gen(8), device="cuda", dtype=torch.int32)
+    at = torch.tensor([0, 1, n // 3, n - 2, n - 1], device="cuda")
+    for out in (torch.empty((cols, n), dtype=torch.float16, device="cuda").t(),
+                torch.empty((n, cols), dtype=torch.float16, device="cuda")):
+        b.gs_lookup(table, ids, out)
+        assert torch.equal(out[at], table[ids[at].long()])
+        del out
+
+
+# ---- gradient ----------------------------------------------------------------
+
+def exact_grad(g, ids, rows, scale):
+    """(sum, sum of sizes, number of terms) per table row in fp64."""
+    g = g.double()
+    ok = ids >= 0
+    at = ids[ok].long()
+    z = torch.zeros((rows, g.shape[1]), dtype=torch.float64, device="cuda")
+    s = z.clone().index_add_(0, at, g[ok])
+    a = z.clone().index_add_(0, at, g[ok].abs())
+    m = torch.bincount(at, minlength=rows).double()[:, None]
+    return scale * s, abs(scale) * a, m
+
+
+def run_grad(b, g, ids, rows, **kw):
+    dt = kw.pop("dtable", None)
+    if dt is None:
+        dt = torch.full((rows, g.shape[1]), 5.0, device="cuda")
+    ws = torch.randint(255, (b.gs_lookup_bwd_workspace_size(g, rows),), dtype=torch.uint8,
+                       generator=gen(11), device="cuda")
+    return b.gs_lookup_bwd(g, ids, dt, ws, **kw)
+
+
+def check_grad(got, ref, slack=0):
+    s, a, m = ref
+    err = (got.double() - s).abs()
+    # m - 1 additions and the scale's product; 1.01 for products of (1 + u)
+    assert (err <= 1.01 * (m + 1 + slack) * U * a + 2.0 ** -149).all(), float((err / (a + 1e-300)).max())
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 33, 64, 65, 257, 1024, 1025, 5000, 40_001, 300_007])
+@pytest.mark.parametrize("cols,kind", [(1, "rows"), (3, "planes"), (4, "rows"), (12, "padded_planes"),
+                                       (27, "rows"), (48, "planes"), (48, "rows"), (16, "padded"),
+                                       (64, "offset"), (130, "planes"), (128, "rows")])
+def test_lookup_gradient(b, n, cols, kind):
+    for k, (dtype, rows, hot, holes) in enumerate([
+            (torch.float32, 1 + n // 3, 0.0, 0.1), (torch.bfloat16, 1, 0.0, 0.0),
+            (torch.float16, 1000, 0.5, 0.02), (torch.float32, 256, 0.9, 0.5),
+            (torch.float32, 70_001, 0.0, 0.0)]):
+        g = torch.randn(n, cols, generator=gen(n + k), device="cuda").to(dtype)
+        ids = make_ids(n, rows, n + cols + k, holes=holes, hot=hot)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        scale = (0.75, 1.0, -2.0)[k % 3]
+        view = layout(g, kind)
+        got = run_grad(b, view, ids, rows, scale=scale, dev_status=st)
+        check_grad(got, exact_grad(g, ids, rows, scale))
+        assert int(st) == 0
+        assert torch.equal(got, run_grad(b, view, ids, rows, scale=scale))  # the same bits again
+
+
+def test_lookup_gradient_is_the_derivative(b):
+    """Central differences of sum(w * lookup): linear in the table, so the
+    difference is exact but for the rounding of its two fp64 sums."""
+    n, rows, cols, scale = 300, 17, 5, 0.75
+    table = torch.randn(rows, cols, generator=gen(21), device="cuda")
+    w = torch.randn(n, cols, generator=gen(22), device="cuda")
+    ids = make_ids(n, rows, 23)
+    got = run_grad(b, w, ids, rows, scale=scale)
+    s, a, m = exact_grad(w, ids, rows, scale)
+
+    def value(t):
+        return (w.double() * b.gs_lookup(t, ids, torch.empty(n, cols, device="cuda"), scale=scale).double()).sum()
+
+    for k, c in ((0, 0), (5, 4), (16, 2)):
+        hi, lo = table.clone(), table.clone()
+        hi[k, c] += 1.0
+        lo[k, c] -= 1.0
+        d = (value(hi) - value(lo)) / (hi[k, c].double() - lo[k, c].double())
+        # each looked-up value rounds by u of its size (at most 1 + |table|)
+        assert abs(float(d - got[k, c])) <= float(2 * U * a[k, c] * (1 + table[k, c].abs())
+                                                  + (m[k, 0] + 1) * U * a[k, c]) + 1e-12
+
+
+def test_lookup_gradient_accumulates_and_keeps_padding(b):
+    n, rows, cols = 3000, 50, 12
+    g = torch.randn(n, cols, generator=gen(31), device="cuda")
+    ids = make_ids(n, rows, 32)
+    ids[ids == 7] = 8  # a row that no item uses
+    buf = torch.full((rows, cols + 3), 2.0, device="cuda")
+    before = torch.randn(rows, cols, generator=gen(33), device="cuda")
+    dt = buf[:, :cols]
+    dt.copy_(before)
+    run_grad(b, g, ids, rows, dtable=dt, scale=0.5, accumulate=True)
+    s, a, m = exact_grad(g, ids, rows, 0.5)
+    check_grad(dt, (s + before.double(), a + before.double().abs(), m), slack=1)
+    assert torch.equal(dt[7], before[7])
+    assert (buf[:, cols:] == 2.0).all()
+    run_grad(b, g, ids, rows, dtable=dt, scale=0.5)
+    check_grad(dt, (s, a, m))
+    assert (dt[7] == 0).all() and (buf[:, cols:] == 2.0).all()
+
+
+@pytest.mark.parametrize("n", [700, 20_000])
+def test_lookup_gradient_with_a_kept_order(b, n):
+    rows, cols = 333, 27
+    ids = make_ids(2 * n, rows, 41)
+    index = torch.randperm(2 * n, generator=gen(42), device="cuda")[:n].sort().values.to(torch.int32)
+    g = torch.randn(cols, n, generator=gen(43), device="cuda").t()
+    ws = torch.empty(b.gs_lookup_bwd_workspace_size(g, rows), dtype=torch.uint8, device="cuda")
+    b.gs_lookup_plan(ids, n, rows, cols, ws, index=index)
+    for k in range(3):
+        gk = g * (k + 1)
+        gk = gk.t().contiguous().t()
+        got = b.gs_lookup_bwd(gk, ids, torch.empty(rows, cols, device="cuda"), ws, index=index, planned=True)
+        check_grad(got, exact_grad(gk, ids[index.long()], rows, 1.0))
+
+
+@pytest.mark.parametrize("n", [200, 30_000])
+def test_lookup_gradient_reads_no_row_without_an_id(b, n):
+    """NaN and infinity in rows whose id is negative or out of range."""
+    rows, cols = 20, 8
+    g = torch.randn(n, cols, generator=gen(51), device="cuda")
+    ids = make_ids(n, rows, 52, holes=0.3)
+    clean = exact_grad(torch.where((ids >= 0)[:, None], g, 0.0), ids, rows, 1.0)
+    g[ids < 0] = float("nan")
+    g[(ids < 0).nonzero()[0]] = float("inf")
+    check_grad(run_grad(b, g, ids, rows), clean)
+    check_grad(run_grad(b, g.t().contiguous().t(), ids, rows), clean)
+    wrong = ids.clone()
+    wrong[(ids < 0).nonzero()[:2]] = rows
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check_grad(run_grad(b, g, wrong, rows, dev_status=st), clean)
+    assert int(st) == 2
+    # every row without an id
+    assert (run_grad(b, g, torch.full_like(ids, -1), rows) == 0).all()
+    # a NaN in a used row stays in its table row
+    ids[5] = 3
+    g[5] = float("nan")
+    got = run_grad(b, g, ids, rows)
+    assert torch.isnan(got[3]).all() and torch.isfinite(got[[0, 1, 2] + list(range(4, rows))]).all()
+
+
+def test_lookup_gradient_of_no_items(b):
+    g = torch.empty((0, 4), device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    dt = torch.ones(3, 4, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    b.gs_lookup_bwd(g, none, dt, ws, accumulate=True)
+    assert (dt == 1).all()
+    b.gs_lookup_bwd(g, none, dt, ws)
+    assert (dt == 0).all()
+
+
+def test_lookup_gradient_past_32_bit_offsets(b):
+    n, cols, rows = 18_000_000, 120, 3
+    g = torch.ones((n, cols), dtype=torch.float16, device="cuda")
+    ids = torch.arange(n, device="cuda", dtype=torch.int32) % rows
+    got = run_grad(b, g, ids, rows)
+    # sums of ones are exact in fp32 up to 2^24
+    assert (got == n // rows).all()
+    del g
+    g = torch.ones((cols, n), dtype=torch.float16, device="cuda").t()
+    assert (run_grad(b, g, ids, rows) == n // rows).all()
+
+
+def test_lookup_on_another_stream_and_in_a_graph(b):
+    """Captured once and replayed with new inputs; on a side stream."""
+    for n, rows, cols in ((50, 9, 16), (20_000, 700, 12)):
+        table = torch.randn(rows, cols, generator=gen(61), device="cuda")
+        ids = make_ids(n, rows, 62)
+        out = torch.empty((cols, n), device="cuda").t()
+        dt = torch.empty(rows, cols, device="cuda")
+        ws = torch.empty(b.gs_lookup_bwd_workspace_size(out, rows), dtype=torch.uint8, device="cuda")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        b.gs_lookup(table, ids, out, stream=side)
+        b.gs_lookup_bwd(out, ids, dt, ws, stream=side)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            b.gs_lookup(table, ids, out, scale=0.5)
+            b.gs_lookup_bwd(out, ids, dt, ws, scale=2.0)
+        for seed in (63, 64):
+            table.copy_(torch.randn(rows, cols, generator=gen(seed), device="cuda"))
+            ids.copy_(make_ids(n, rows, seed))
+            graph.replay()
+            got_out, got_dt = out.clone(), dt.clone()
+            want_out = b.gs_lookup(table, ids, torch.empty_like(out), scale=0.5)
+            assert torch.equal(got_out, want_out)
+            assert torch.equal(got_dt, run_grad(b, want_out.t().contiguous().t(), ids, rows, scale=2.0))
+
+
+def test_lookup_capacity(b):
+    g = torch.ones(5000, 8, device="cuda")
+    ids = make_ids(5000, 10, 71)
+    ws = torch.empty(b.gs_lookup_bwd_workspace_size(g, 10) - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(b.GsError) as e:
+        b.gs_lookup_bwd(g, ids, torch.empty(10, 8, device="cuda"), ws)
+    assert e.value.status == b.GS_ERR_CAPACITY
