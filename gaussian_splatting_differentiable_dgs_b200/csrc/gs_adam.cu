@@ -264,20 +264,87 @@ k_adam(float* __restrict__ P, float* __restrict__ m, float* __restrict__ v,
   }
 }
 
+// p -= lr (m / bc1) / (sqrt(v / bc2) + eps), with the bias corrections
+// folded into two host-computed factors and one fast division (2 ulp).
+__device__ __forceinline__ void adam_vals(float& p, float& m, float& v, float g, const AdamK& a) {
+  m = fmaf(a.b1, m, a.omb1 * g);
+  v = fmaf(a.b2, v, a.omb2 * g * g);
+  p = fmaf(-a.step, __fdividef(m, fmaf(sqrtf(v), a.rsbc2, a.eps)), p);
+}
+
 // Adam on the clipped gradient: g is scaled by the coefficient clip[1] of
-// gs_grad_norm as it is read, so clipping costs no pass of its own.
+// gs_grad_norm as it is read, so clipping costs no pass of its own.  A thread
+// owns V neighbouring Gaussians (one 16-byte vector of p, m and v each where
+// the planes allow it) in kAdamPlanes planes; all loads of its planes are
+// issued before the first is used.
+constexpr int kAdamPlanes = 4;
+
+template <int V>
 __global__ void __launch_bounds__(kThreads)
 k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__ v,
                const float* __restrict__ g, int64_t g_stride, const int32_t* __restrict__ slot,
-               int64_t n, int64_t n_pad, int nP, const float* __restrict__ clip, AdamK a) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+               bool g_vec, int64_t n, int64_t n_pad, int nP, unsigned col_blocks,
+               const float* __restrict__ clip, AdamK a) {
+  const int64_t i = ((int64_t)(blockIdx.x % col_blocks) * kThreads + threadIdx.x) * V;
   if (i >= n) return;
+  const int plane0 = (int)(blockIdx.x / col_blocks) * kAdamPlanes;
+  const int cnt = n - i < V ? (int)(n - i) : V;
   const float c = clip[1];
-  const int64_t col = slot ? slot[i] : i;
-  const bool has = col >= 0 && col < g_stride;
-  for (int plane = 0; plane < nP; ++plane) {
-    const float gg = has ? c * g[(int64_t)plane * g_stride + col] : 0.0f;
-    adam_update(P, m, v, (int64_t)plane * n_pad + i, gg, a);
+  int64_t col[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    col[k] = k < cnt ? (slot ? (int64_t)slot[i + k] : i + k) : -1;
+    if (col[k] >= g_stride) col[k] = -1;
+  }
+  float pp[kAdamPlanes][V], mm[kAdamPlanes][V], vv[kAdamPlanes][V], gg[kAdamPlanes][V];
+#pragma unroll
+  for (int q = 0; q < kAdamPlanes; ++q) {
+    if (plane0 + q >= nP) break;
+    const int64_t at = (int64_t)(plane0 + q) * n_pad + i;
+    const float* gp = g + (int64_t)(plane0 + q) * g_stride;
+    if (V == 4 && cnt == 4) {
+      *reinterpret_cast<float4*>(pp[q]) = *reinterpret_cast<const float4*>(P + at);
+      *reinterpret_cast<float4*>(mm[q]) = *reinterpret_cast<const float4*>(m + at);
+      *reinterpret_cast<float4*>(vv[q]) = *reinterpret_cast<const float4*>(v + at);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (k < cnt) {
+          pp[q][k] = P[at + k];
+          mm[q][k] = m[at + k];
+          vv[q][k] = v[at + k];
+        }
+    }
+    if (V == 4 && cnt == 4 && g_vec) {
+      *reinterpret_cast<float4*>(gg[q]) = __ldg(reinterpret_cast<const float4*>(gp + i));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) gg[q][k] = col[k] >= 0 ? gp[col[k]] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kAdamPlanes; ++q) {
+    if (plane0 + q >= nP) break;
+    const int64_t at = (int64_t)(plane0 + q) * n_pad + i;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      // a Gaussian without a gradient takes 0, also where c is not finite
+      const float x = col[k] >= 0 ? c * gg[q][k] : 0.0f;
+      adam_vals(pp[q][k], mm[q][k], vv[q][k], x, a);
+    }
+    if (V == 4 && cnt == 4) {
+      *reinterpret_cast<float4*>(P + at) = *reinterpret_cast<const float4*>(pp[q]);
+      *reinterpret_cast<float4*>(m + at) = *reinterpret_cast<const float4*>(mm[q]);
+      *reinterpret_cast<float4*>(v + at) = *reinterpret_cast<const float4*>(vv[q]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (k < cnt) {
+          P[at + k] = pp[q][k];
+          m[at + k] = mm[q][k];
+          v[at + k] = vv[q][k];
+        }
+    }
   }
 }
 
@@ -350,14 +417,6 @@ __device__ __forceinline__ void sh_term(int k, double x, double y, double z, dou
     default: Y = -k3a * x * (xx - 3.0 * yy); Yx = -3.0 * k3a * (xx - yy); Yy = 6.0 * k3a * x * y;
              Yz = 0.0; break;
   }
-}
-
-// p -= lr (m / bc1) / (sqrt(v / bc2) + eps), with the bias corrections
-// folded into two host-computed factors and one fast division (2 ulp).
-__device__ __forceinline__ void adam_vals(float& p, float& m, float& v, float g, const AdamK& a) {
-  m = fmaf(a.b1, m, a.omb1 * g);
-  v = fmaf(a.b2, v, a.omb2 * g * g);
-  p = fmaf(-a.step, __fdividef(m, fmaf(sqrtf(v), a.rsbc2, a.eps)), p);
 }
 
 // Fused path, stage 2, staged through shared memory: a CTA owns kThreads
@@ -724,8 +783,20 @@ extern "C" gs_status gs_adam_clipped(float* params, float* m, float* v, const fl
   if (n == 0) return GS_OK;
   if (!params || !m || !v || !g || !clip) return GS_ERR_ARG;
   if (!slot && g_stride < n) return GS_ERR_ARG;
-  k_adam_clipped<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, to_stream(stream)>>>(
-      params, m, v, g, g_stride, slot, n, n_pad, P, clip, a);
+  // 16-byte vectors of p, m and v need planes and addresses that keep them
+  // aligned; without them a thread owns one Gaussian
+  const bool vec = (n_pad & 3) == 0 && aligned(params, 16) && aligned(m, 16) && aligned(v, 16);
+  const bool g_vec = !slot && (g_stride & 3) == 0 && aligned(g, 16);
+  const int64_t threads = vec ? (n + 3) / 4 : n;
+  const int64_t col_blocks = (threads + kThreads - 1) / kThreads;
+  const int64_t blocks = col_blocks * ((P + (int64_t)kAdamPlanes - 1) / kAdamPlanes);
+  if (blocks > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
+  if (vec)
+    k_adam_clipped<4><<<(unsigned)blocks, kThreads, 0, to_stream(stream)>>>(
+        params, m, v, g, g_stride, slot, g_vec, n, n_pad, P, (unsigned)col_blocks, clip, a);
+  else
+    k_adam_clipped<1><<<(unsigned)blocks, kThreads, 0, to_stream(stream)>>>(
+        params, m, v, g, g_stride, slot, false, n, n_pad, P, (unsigned)col_blocks, clip, a);
   GS_LAUNCH_CHECK();
   return GS_OK;
 }

@@ -15,9 +15,12 @@ namespace gs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 8192;      // elements a block takes at a time
-constexpr int kMaxTensors = 256;  // tensors per launch, passed by value
-constexpr int kNormBlocks = 148 * 4;
+constexpr int kUnitBytes = 16384;  // bytes of a row that a block takes at a time
+constexpr int kFlatUnit = 4096;    // elements, where rows are too short for that
+constexpr int kShortRow = 1024;    // columns below which rows are short
+constexpr int kMaxTensors = 256;   // tensors per launch, passed by value
+constexpr int kNormBlocks = 148 * 8;
+constexpr int kClipBlocks = 148 * 8;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -26,11 +29,20 @@ __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// 16 bytes of elements
+template <class T>
+union Vec {
+  uint4 raw;
+  T x[16 / sizeof(T)];
+  __device__ Vec() {}
+};
+
 struct Entry {
   const void* src;
   void* dst;
   int64_t cols, src_stride, dst_stride, size;  // size = rows * cols
   int64_t unit0;                               // first unit of this tensor
+  int32_t row_units;                           // units per row; 0: rows are short
   int32_t dtype;
 };
 
@@ -40,30 +52,57 @@ struct Table {
   int64_t units;
 };
 
-// Calls f(typed src, typed dst, element offset in src, in dst) for this
-// thread's elements of unit u.
+constexpr int kVecs = kUnitBytes / 16 / kThreads;  // vectors of a unit per thread
+
+// Unit u of tensor e: a stretch of one row, cut into single elements up to
+// the source's first 16-byte boundary, vectors, and the rest.
+template <class T>
+struct Stretch {
+  const T* src;
+  T* dst;
+  int len, head, nv;
+  __device__ Stretch(const Entry& e, int64_t u) {
+    constexpr int V = 16 / sizeof(T), kUnit = kUnitBytes / sizeof(T);
+    u -= e.unit0;
+    const int64_t r = u / e.row_units, c0 = (u - r * e.row_units) * kUnit;
+    len = (int)min((int64_t)kUnit, e.cols - c0);
+    src = static_cast<const T*>(e.src) + r * e.src_stride + c0;
+    dst = static_cast<T*>(e.dst) + r * e.dst_stride + c0;
+    head = min(len, (int)(((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / sizeof(T)));
+    nv = (len - head) / V;
+  }
+  // one(i): this thread's single elements before and behind the vectors
+  template <class F>
+  __device__ __forceinline__ void ends(F&& one) const {
+    const int t = threadIdx.x, tail = head + nv * (16 / (int)sizeof(T));
+    if (t < head) one(t);
+    if (t < len - tail) one(tail + t);
+  }
+};
+
+// Unit u of a tensor with short rows: single elements, with a division each.
 template <class T, class F>
-__device__ __forceinline__ void unit_elements(const Entry& e, int64_t u, F&& f) {
-  const T* src = static_cast<const T*>(e.src);
-  T* dst = static_cast<T*>(e.dst);
-  const int64_t a = (u - e.unit0) * kUnit, b = min(a + kUnit, e.size);
+__device__ __forceinline__ void short_rows(const Entry& e, int64_t u, F&& one) {
+  const int64_t a = (u - e.unit0) * kFlatUnit, b = min(a + kFlatUnit, e.size);
   for (int64_t i = a + threadIdx.x; i < b; i += kThreads) {
     const int64_t r = i / e.cols, c = i - r * e.cols;
-    f(src, dst, r * e.src_stride + c, r * e.dst_stride + c);
+    one(static_cast<const T*>(e.src) + r * e.src_stride + c,
+        static_cast<T*>(e.dst) + r * e.dst_stride + c);
   }
 }
 
-template <class F>
+// f(tensor, unit) for this block's units, in turn from the first or the last
+template <bool BACK, class F>
 __device__ __forceinline__ void each_unit(const Table& tab, F&& f) {
-  for (int64_t u = blockIdx.x; u < tab.units; u += gridDim.x) {
+  for (int64_t k = blockIdx.x; k < tab.units; k += gridDim.x) {
+    const int64_t u = BACK ? tab.units - 1 - k : k;
     int lo = 0, hi = tab.count - 1;  // the last tensor with unit0 <= u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (tab.t[mid].unit0 <= u) lo = mid;
       else hi = mid - 1;
     }
-    const Entry& e = tab.t[lo];
-    f(e, u);
+    f(tab.t[lo], u);
   }
 }
 
@@ -74,14 +113,29 @@ __global__ void __launch_bounds__(kThreads)
 k_sum_squares(const __grid_constant__ Table tab, double* __restrict__ part) {
   __shared__ double s_warp[kThreads / 32];
   double sum = 0.0;
-  each_unit(tab, [&](const Entry& e, int64_t u) {
-    auto add = [&](auto* src, auto*, int64_t at, int64_t) {
-      const double x = (double)to_f(src[at]);
-      sum = fma(x, x, sum);
-    };
-    if (e.dtype == GS_F32) unit_elements<float>(e, u, add);
-    else if (e.dtype == GS_F16) unit_elements<__half>(e, u, add);
-    else unit_elements<__nv_bfloat16>(e, u, add);
+  auto unit = [&](auto zero, const Entry& e, int64_t u) {
+    using T = decltype(zero);
+    constexpr int V = 16 / sizeof(T);
+    auto add = [&](float x) { sum = fma((double)x, (double)x, sum); };
+    if (e.row_units == 0) return short_rows<T>(e, u, [&](const T* p, T*) { add(to_f(*p)); });
+    const Stretch<T> x(e, u);
+    Vec<T> buf[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      buf[k].raw = i < x.nv ? __ldg(reinterpret_cast<const uint4*>(x.src + x.head) + i)
+                            : make_uint4(0, 0, 0, 0);
+    }
+    x.ends([&](int i) { add(to_f(x.src[i])); });
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) add(to_f(buf[k].x[i]));
+  };
+  each_unit<false>(tab, [&](const Entry& e, int64_t u) {
+    if (e.dtype == GS_F32) unit(0.f, e, u);
+    else if (e.dtype == GS_F16) unit(__half(), e, u);
+    else unit(__nv_bfloat16(), e, u);
   });
   sum = warp_sum(sum);
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = sum;
@@ -112,15 +166,45 @@ k_clip_coef(const double* __restrict__ part, int n, double max_norm, double eps,
   }
 }
 
+// The units are taken from the last to the first: what the norm read last is
+// still in L2.
 __global__ void __launch_bounds__(kThreads)
 k_clip(const __grid_constant__ Table tab, const float* __restrict__ clip) {
   const float c = clip[1];
-  each_unit(tab, [&](const Entry& e, int64_t u) {
+  auto unit = [&](auto zero, const Entry& e, int64_t u) {
+    using T = decltype(zero);
+    constexpr int V = 16 / sizeof(T);
+    if (e.row_units == 0)
+      return short_rows<T>(e, u, [&](const T* p, T* q) { put(q, c * to_f(*p)); });
+    const Stretch<T> x(e, u);
+    const bool aligned_dst = (reinterpret_cast<uintptr_t>(x.dst + x.head) & 15) == 0;
+    Vec<T> buf[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < x.nv) buf[k].raw = *(reinterpret_cast<const uint4*>(x.src + x.head) + i);
+    }
+    x.ends([&](int i) { put(x.dst + i, c * to_f(x.src[i])); });
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i >= x.nv) break;
+      Vec<T> w;
+#pragma unroll
+      for (int j = 0; j < V; ++j) put(&w.x[j], c * to_f(buf[k].x[j]));
+      if (aligned_dst) {
+        *(reinterpret_cast<uint4*>(x.dst + x.head) + i) = w.raw;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x.dst[x.head + i * V + j] = w.x[j];
+      }
+    }
+  };
+  each_unit<true>(tab, [&](const Entry& e, int64_t u) {
     if (c == 1.0f && e.src == e.dst) return;  // in place and nothing to clip
-    auto scale = [&](auto* src, auto* dst, int64_t at, int64_t to) { put(dst + to, c * to_f(src[at])); };
-    if (e.dtype == GS_F32) unit_elements<float>(e, u, scale);
-    else if (e.dtype == GS_F16) unit_elements<__half>(e, u, scale);
-    else unit_elements<__nv_bfloat16>(e, u, scale);
+    if (e.dtype == GS_F32) unit(0.f, e, u);
+    else if (e.dtype == GS_F16) unit(__half(), e, u);
+    else unit(__nv_bfloat16(), e, u);
   });
 }
 
@@ -166,8 +250,9 @@ bool pair_up(gs_tensor* a, gs_tensor* b) {
   return a->rows == b->rows && a->cols == b->cols;
 }
 
-// Fills tab with up to kMaxTensors non-empty tensors from *at on.
-void fill(Table& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count, int32_t* at) {
+// Fills tab with up to kMaxTensors non-empty tensors from *at on; false if one
+// has rows of more units than 32 bits count.
+bool fill(Table& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count, int32_t* at) {
   tab.count = 0;
   tab.units = 0;
   for (; *at < count && tab.count < kMaxTensors; ++*at) {
@@ -183,8 +268,13 @@ void fill(Table& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count,
     e.src_stride = t.row_stride;
     e.dst_stride = d.row_stride;
     e.unit0 = tab.units;
-    tab.units += (e.size + kUnit - 1) / kUnit;
+    const int64_t unit = kUnitBytes / (int64_t)type_size(t.dtype);
+    const int64_t row_units = (t.cols + unit - 1) / unit;
+    if (row_units > INT32_MAX) return false;
+    e.row_units = t.rows > 1 && t.cols < kShortRow ? 0 : (int32_t)row_units;
+    tab.units += e.row_units ? t.rows * row_units : (e.size + kFlatUnit - 1) / kFlatUnit;
   }
+  return true;
 }
 
 }  // namespace
@@ -210,7 +300,7 @@ extern "C" gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, doubl
   int parts = 0;
   static thread_local Table tab;
   for (int32_t at = 0; at < count;) {
-    fill(tab, tensors, nullptr, count, &at);
+    if (!fill(tab, tensors, nullptr, count, &at)) return GS_ERR_UNSUPPORTED;
     if (tab.count == 0) break;
     const unsigned blocks = (unsigned)(tab.units < kNormBlocks ? tab.units : kNormBlocks);
     k_sum_squares<<<blocks, kThreads, 0, s>>>(tab, part + parts);
@@ -238,9 +328,9 @@ extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, in
   cudaStream_t s = to_stream(stream);
   static thread_local Table tab;
   for (int32_t at = 0; at < count;) {
-    fill(tab, src, dst, count, &at);
+    if (!fill(tab, src, dst, count, &at)) return GS_ERR_UNSUPPORTED;
     if (tab.count == 0) break;
-    const unsigned blocks = (unsigned)(tab.units < 148 * 16 ? tab.units : 148 * 16);
+    const unsigned blocks = (unsigned)(tab.units < kClipBlocks ? tab.units : kClipBlocks);
     k_clip<<<blocks, kThreads, 0, s>>>(tab, clip);
     GS_LAUNCH_CHECK();
   }
