@@ -51,19 +51,118 @@ __device__ __forceinline__ int32_t id_of(const int32_t* __restrict__ ids, int64_
   return id;
 }
 
-// One thread per element of out; the contiguous axis of out runs fastest.
-template <class TT, class TO>
+// V elements of the table's type as one load of V * sizeof(T) bytes
+template <class T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T x[V];
+};
+
+// Division by a number fixed at launch, for dividends below 2^31:
+// q = (x * m) >> 32 >> s with m = ceil(2^(32+s) / d), s = ceil(log2 d) - 1
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994); d = 1 is left out by the caller's `one`.
+struct Div {
+  uint32_t d, m, s;
+  __host__ explicit Div(uint32_t dd) : d(dd), m(0), s(0) {
+    if (d <= 1) return;
+    while ((2ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << (32 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t quot(uint32_t x) const {
+    return d == 1 ? x : __umulhi(x, m) >> s;
+  }
+};
+
+// out in rows: one thread per V columns of an item, kRowIlp items' vectors in
+// flight.  A block takes kThreads * kRowIlp consecutive vectors.
+constexpr int kRowIlp = 4;
+template <class TT, class TO, int V>
 __global__ void __launch_bounds__(kThreads)
-k_lookup(const TT* __restrict__ table, int64_t ld, int64_t rows, const int32_t* __restrict__ ids,
-         int64_t n_ids, const int32_t* __restrict__ index, float scale, TO* __restrict__ out,
-         int64_t n, int cols, int64_t rs, int64_t cs, int32_t* dev_status) {
-  const int64_t total = n * cols, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += step) {
-    const int64_t j = cs == 1 ? e / cols : e % n;
-    const int64_t c = cs == 1 ? e % cols : e / n;
-    const int32_t id = id_of(ids, n_ids, index, j, rows, dev_status);
-    const float v = id >= 0 ? scale * to_f(table[(int64_t)id * ld + c]) : 0.f;
-    out[j * rs + c * cs] = from_f<TO>(v);
+k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
+              const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
+              float scale, TO* __restrict__ out, int64_t n, int64_t rs, Div nv, int items,
+              int32_t* dev_status) {
+  const int64_t j0 = (int64_t)blockIdx.x * items;  // items per block
+  const uint32_t total = (uint32_t)min((int64_t)items, n - j0) * nv.d;
+  for (uint32_t e0 = threadIdx.x; e0 < total; e0 += kThreads * kRowIlp) {
+    Pack<TT, V> in[kRowIlp];
+    uint32_t at[kRowIlp], c[kRowIlp];
+    bool has[kRowIlp];
+#pragma unroll
+    for (int k = 0; k < kRowIlp; ++k) {
+      const uint32_t e = min(e0 + k * kThreads, total - 1);
+      at[k] = nv.quot(e);
+      c[k] = (e - at[k] * nv.d) * V;
+      const int32_t id = id_of(ids, n_ids, index, j0 + at[k], rows, dev_status);
+      has[k] = id >= 0;
+      if (has[k])
+        in[k] = *reinterpret_cast<const Pack<TT, V>*>(table + (int64_t)id * ld + c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowIlp; ++k) {
+      if (e0 + k * kThreads >= total) break;
+      Pack<TO, V> w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w.x[i] = from_f<TO>(has[k] ? scale * to_f(in[k].x[i]) : 0.f);
+      *reinterpret_cast<Pack<TO, V>*>(out + (j0 + at[k]) * rs + c[k]) = w;
+    }
+  }
+}
+
+// out in planes: a block gathers kTileItems rows (up to kTileCols columns of
+// them) with loads along the rows, turns them in shared memory and writes
+// along the planes.  The pitch kTileItems + 1 spreads the columns of one row
+// over the banks.
+constexpr int kTileItems = 128, kTileCols = 48, kTilePitch = kTileItems + 1;
+template <class TT, class TO, int V>
+__global__ void __launch_bounds__(kThreads)
+k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows,
+                const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
+                float scale, TO* __restrict__ out, int64_t n, int64_t cs, int cols, int per,
+                unsigned col_tiles, int32_t* dev_status) {
+  extern __shared__ float s_tile[];  // [per][kTilePitch]
+  __shared__ int32_t s_id[kTileItems];
+  const int64_t j0 = (int64_t)(blockIdx.x / col_tiles) * kTileItems;
+  const int c0 = (int)(blockIdx.x % col_tiles) * per;
+  const int items = (int)min((int64_t)kTileItems, n - j0), width = min(per, cols - c0);
+  const int t = threadIdx.x;
+  if (t < items) s_id[t] = id_of(ids, n_ids, index, j0 + t, rows, dev_status);
+  __syncthreads();
+  const int nv = width / V, total = items * nv;
+  table += c0;
+  // t / nv and t % nv of successive e = t + k * kThreads without a division
+  int j = t / nv, q = t - j * nv;
+  const int dj = kThreads / nv, dq = kThreads - dj * nv;
+  for (int e = t; e < total; e += 4 * kThreads) {
+    Pack<TT, V> in[4];
+    int jj[4], qq[4];
+    int32_t id[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      jj[k] = j;
+      qq[k] = q;
+      j += dj;
+      q += dq;
+      if (q >= nv) {
+        q -= nv;
+        ++j;
+      }
+      id[k] = e + k * kThreads < total ? s_id[jj[k]] : -1;
+      if (id[k] >= 0)
+        in[k] = *reinterpret_cast<const Pack<TT, V>*>(table + (int64_t)id[k] * ld + qq[k] * V);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (e + k * kThreads >= total) break;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        s_tile[(qq[k] * V + i) * kTilePitch + jj[k]] = id[k] >= 0 ? scale * to_f(in[k].x[i]) : 0.f;
+    }
+  }
+  __syncthreads();
+  for (int c = t / kTileItems; c < width; c += kThreads / kTileItems) {
+    const int jw = t % kTileItems;
+    if (jw < items) out[(int64_t)(c0 + c) * cs + j0 + jw] = from_f<TO>(s_tile[c * kTilePitch + jw]);
   }
 }
 
@@ -224,24 +323,67 @@ gs_status run_sums(const gs_matrix* g, const gs_matrix* dtable, float scale, boo
   return GS_OK;
 }
 
-template <class TT, class TO>
+// Elements of size es that may move together: a divisor of cols and the
+// stride that keeps every vector of the matrix aligned, at most `most`.
+int vector_of(const void* p, int64_t ld, int cols, int es, int most) {
+  int v = most;
+  while (v > 1 && (cols % v || ld % v || !aligned(p, (size_t)v * es))) v >>= 1;
+  return v;
+}
+
+template <class TT, class TO, int V>
 gs_status launch_lookup(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
                         float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
-  const int64_t blocks = (o->rows * o->cols + kThreads - 1) / kThreads;
-  k_lookup<TT, TO><<<(unsigned)(blocks < 148 * 64 ? blocks : 148 * 64), kThreads, 0, s>>>(
-      static_cast<const TT*>(t->data), t->row_stride, t->rows, ids, n_ids, index, scale,
-      static_cast<TO*>(o->data), o->rows, o->cols, o->row_stride, o->col_stride, dev_status);
+  const TT* table = static_cast<const TT*>(t->data);
+  TO* out = static_cast<TO*>(o->data);
+  const int cols = o->cols;
+  if (o->col_stride == 1) {
+    constexpr int VR = V * sizeof(TO) <= 16 ? V : 16 / sizeof(TO);  // a store has 16 bytes at most
+    const int nv = cols / VR;
+    int items = kThreads * kRowIlp / nv;
+    if (items < 1) items = 1;
+    const int64_t blocks = (o->rows + items - 1) / items;
+    k_lookup_rows<TT, TO, VR><<<(unsigned)blocks, kThreads, 0, s>>>(
+        table, t->row_stride, t->rows, ids, n_ids, index, scale, out, o->rows, o->row_stride,
+        Div((uint32_t)nv), items, dev_status);
+  } else {
+    // columns per block: all of up to kTileCols, else equal shares that V divides
+    const int tiles = (cols + kTileCols - 1) / kTileCols;
+    const int per = (((cols + tiles - 1) / tiles) + V - 1) / V * V;
+    const unsigned col_tiles = (unsigned)((cols + per - 1) / per);
+    const int64_t blocks = (o->rows + kTileItems - 1) / kTileItems * col_tiles;
+    if (blocks > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
+    const size_t smem = sizeof(float) * per * kTilePitch;
+    k_lookup_planes<TT, TO, V><<<(unsigned)blocks, kThreads, smem, s>>>(
+        table, t->row_stride, t->rows, ids, n_ids, index, scale, out, o->rows, o->col_stride, cols,
+        per, col_tiles, dev_status);
+  }
   GS_LAUNCH_CHECK();
   return GS_OK;
+}
+
+template <class TT, class TO>
+gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
+                    float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
+  constexpr int most = 16 / sizeof(TT);
+  int v = vector_of(t->data, t->row_stride, t->cols, sizeof(TT), most);
+  if (o->col_stride == 1) {  // both sides move V elements at a time
+    const int vo = vector_of(o->data, o->row_stride, o->cols, sizeof(TO), 16 / sizeof(TO));
+    if (vo < v) v = vo;
+  }
+  if (v == 8 && most >= 8) return launch_lookup<TT, TO, most >= 8 ? 8 : 1>(t, ids, n_ids, index, scale, o, dev_status, s);
+  if (v == 4) return launch_lookup<TT, TO, 4>(t, ids, n_ids, index, scale, o, dev_status, s);
+  if (v == 2) return launch_lookup<TT, TO, 2>(t, ids, n_ids, index, scale, o, dev_status, s);
+  return launch_lookup<TT, TO, 1>(t, ids, n_ids, index, scale, o, dev_status, s);
 }
 
 template <class TT>
 gs_status lookup_to(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
                     float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
   switch (o->dtype) {
-    case GS_F32: return launch_lookup<TT, float>(t, ids, n_ids, index, scale, o, dev_status, s);
-    case GS_F16: return launch_lookup<TT, __half>(t, ids, n_ids, index, scale, o, dev_status, s);
-    default: return launch_lookup<TT, __nv_bfloat16>(t, ids, n_ids, index, scale, o, dev_status, s);
+    case GS_F32: return lookup_by<TT, float>(t, ids, n_ids, index, scale, o, dev_status, s);
+    case GS_F16: return lookup_by<TT, __half>(t, ids, n_ids, index, scale, o, dev_status, s);
+    default: return lookup_by<TT, __nv_bfloat16>(t, ids, n_ids, index, scale, o, dev_status, s);
   }
 }
 
