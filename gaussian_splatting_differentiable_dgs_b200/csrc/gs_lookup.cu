@@ -109,60 +109,117 @@ k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
   }
 }
 
-// out in planes: a block gathers kTileItems rows (up to kTileCols columns of
-// them) with loads along the rows, turns them in shared memory and writes
-// along the planes.  The pitch kTileItems + 1 spreads the columns of one row
-// over the banks.
-constexpr int kTileItems = 128, kTileCols = 48, kTilePitch = kTileItems + 1;
-template <class TT, class TO, int V>
-__global__ void __launch_bounds__(kThreads)
-k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows,
-                const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
-                float scale, TO* __restrict__ out, int64_t n, int64_t cs, int cols, int per,
-                unsigned col_tiles, int32_t* dev_status) {
-  extern __shared__ float s_tile[];  // [per][kTilePitch]
-  __shared__ int32_t s_id[kTileItems];
-  const int64_t j0 = (int64_t)(blockIdx.x / col_tiles) * kTileItems;
-  const int c0 = (int)(blockIdx.x % col_tiles) * per;
-  const int items = (int)min((int64_t)kTileItems, n - j0), width = min(per, cols - c0);
-  const int t = threadIdx.x;
-  if (t < items) s_id[t] = id_of(ids, n_ids, index, j0 + t, rows, dev_status);
-  __syncthreads();
-  const int nv = width / V, total = items * nv;
-  table += c0;
-  // t / nv and t % nv of successive e = t + k * kThreads without a division
-  int j = t / nv, q = t - j * nv;
-  const int dj = kThreads / nv, dq = kThreads - dj * nv;
-  for (int e = t; e < total; e += 4 * kThreads) {
-    Pack<TT, V> in[4];
-    int jj[4], qq[4];
-    int32_t id[4];
+// out in planes: one thread per item.  It loads up to NW 32-bit words of its
+// row (a share of the columns) into registers in 16-byte vectors, all in
+// flight at once, and the warp writes 32 neighbouring items of a plane with
+// each store: no shared memory, no barrier.
+//
+// Rows that do not start on 16 bytes are covered by the aligned vectors that
+// they touch and moved into place by selects (by 2 words, by 1, by half a
+// word).  Vectors that reach over the table's first or last byte are read by
+// element.
+template <class TT>
+__device__ __forceinline__ uint4 load_cover(uintptr_t p, uintptr_t first, uintptr_t last) {
+  if (p >= first && p + 16 <= last) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      jj[k] = j;
-      qq[k] = q;
-      j += dj;
-      q += dq;
-      if (q >= nv) {
-        q -= nv;
-        ++j;
-      }
-      id[k] = e + k * kThreads < total ? s_id[jj[k]] : -1;
-      if (id[k] >= 0)
-        in[k] = *reinterpret_cast<const Pack<TT, V>*>(table + (int64_t)id[k] * ld + qq[k] * V);
-    }
+  for (int i = 0; i < (int)(16 / sizeof(TT)); ++i) {
+    const uintptr_t q = p + i * sizeof(TT);
+    if (q < first || q >= last) continue;
+    if (sizeof(TT) == 4) w[i] = *reinterpret_cast<const uint32_t*>(q);
+    else w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(q) << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class TT>
+__device__ __forceinline__ float element(const uint32_t* w, int c);
+template <>
+__device__ __forceinline__ float element<float>(const uint32_t* w, int c) {
+  return __uint_as_float(w[c]);
+}
+template <>
+__device__ __forceinline__ float element<__half>(const uint32_t* w, int c) {
+  return __half2float(__ushort_as_half((unsigned short)(w[c / 2] >> (16 * (c & 1)))));
+}
+template <>
+__device__ __forceinline__ float element<__nv_bfloat16>(const uint32_t* w, int c) {
+  return __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
+}
+
+// 32 bytes as one load (one whole sector of L2 and L1)
+__device__ __forceinline__ void load_32(uint32_t* w, const void* p) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+      : "l"(p));
+}
+
+// NW words of a row from column c0 on (`width` of its columns if !FULL)
+template <class TT, int NW, int ALIGNED, bool FULL>
+__device__ __forceinline__ void load_words(uint32_t* w, const TT* table, int64_t ld, int64_t rows,
+                                           int table_cols, int64_t id, int c0, int width) {
+  constexpr int E = 4 / sizeof(TT), NL = ALIGNED ? NW : NW + 4;
+  const uintptr_t first = reinterpret_cast<uintptr_t>(table);
+  const uintptr_t row = first + (uintptr_t)(id * ld + c0) * sizeof(TT);
+  if (ALIGNED == 32) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (e + k * kThreads >= total) break;
+    for (int v = 0; v < NW / 8; ++v)
+      if (FULL || v * 8 * E < width) load_32(w + 8 * v, reinterpret_cast<const uint4*>(row) + 2 * v);
+  } else if (ALIGNED == 16) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        s_tile[(qq[k] * V + i) * kTilePitch + jj[k]] = id[k] >= 0 ? scale * to_f(in[k].x[i]) : 0.f;
+    for (int v = 0; v < NW / 4; ++v)
+      if (FULL || v * 4 * E < width)
+        *reinterpret_cast<uint4*>(w + 4 * v) = __ldg(reinterpret_cast<const uint4*>(row) + v);
+  } else {
+    const uintptr_t last = first + (uintptr_t)((rows - 1) * ld + table_cols) * sizeof(TT);
+    const uintptr_t p = row & ~(uintptr_t)15, end = row + (uintptr_t)width * sizeof(TT);
+#pragma unroll
+    for (int v = 0; v < NL / 4; ++v)
+      if (p + 16 * v < end)
+        *reinterpret_cast<uint4*>(w + 4 * v) = load_cover<TT>(p + 16 * v, first, last);
+    const unsigned o = (unsigned)(row & 15);
+#pragma unroll
+    for (int k = 0; k + 2 < NL; ++k) w[k] = o & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k + 3 < NL; ++k) w[k] = o & 4 ? w[k + 1] : w[k];
+    if (E == 2) {
+      const unsigned sh = (o & 2) * 8;
+#pragma unroll
+      for (int k = 0; k + 4 < NL; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], sh);
     }
   }
-  __syncthreads();
-  for (int c = t / kTileItems; c < width; c += kThreads / kTileItems) {
-    const int jw = t % kTileItems;
-    if (jw < items) out[(int64_t)(c0 + c) * cs + j0 + jw] = from_f<TO>(s_tile[c * kTilePitch + jw]);
+}
+
+template <class TT, class TO, int NW, int ALIGNED>
+__global__ void __launch_bounds__(kThreads, NW > 16 ? 3 : 5)
+k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int table_cols,
+                const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
+                float scale, TO* __restrict__ out, int64_t n, int64_t cs, int32_t* dev_status) {
+  constexpr int C = NW * 4 / sizeof(TT);           // columns at a time
+  constexpr int NL = ALIGNED ? NW : NW + 4;        // words loaded
+  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (j >= n) return;
+  const int32_t id = id_of(ids, n_ids, index, j, rows, dev_status);
+  const bool has = id >= 0;
+  TO* o = out + j;
+  uint32_t w[NL];
+  const auto store = [&](int c) {
+    *o = from_f<TO>(has ? scale * element<TT>(w, c) : 0.f);
+    o += cs;
+    asm volatile("" : "+l"(o));  // one running pointer, not C addresses in registers
+  };
+  int c0 = 0;
+  for (; c0 + C <= table_cols; c0 += C) {
+    load_words<TT, NW, ALIGNED, true>(w, table, ld, rows, table_cols, has ? id : 0, c0, C);
+#pragma unroll
+    for (int c = 0; c < C; ++c) store(c);
+  }
+  if (c0 < table_cols) {
+    const int width = table_cols - c0;
+    load_words<TT, NW, ALIGNED, false>(w, table, ld, rows, table_cols, has ? id : 0, c0, width);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (c < width) store(c);
   }
 }
 
@@ -240,6 +297,8 @@ k_run_sums(const uint32_t* __restrict__ keys, const int32_t* __restrict__ order,
   }
 }
 
+unsigned blocks_for(int64_t threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
+
 int key_bits(int64_t rows) { return rows > 1 ? 64 - __builtin_clzll((unsigned long long)(rows - 1)) : 0; }
 
 constexpr int kChunk = 64;  // entries per chunk
@@ -291,8 +350,6 @@ gs_status check_ids(const int32_t* ids, int64_t n_ids, const int32_t* index, int
   return GS_OK;
 }
 
-unsigned blocks_for(int64_t threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
-
 gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, int64_t n,
                       int64_t rows, const LookupWs& w, int32_t* dev_status, cudaStream_t s) {
   k_lookup_keys<<<blocks_for(n), kThreads, 0, s>>>(ids, n_ids, index, n, rows, w.keys, w.order,
@@ -332,32 +389,15 @@ int vector_of(const void* p, int64_t ld, int cols, int es, int most) {
 }
 
 template <class TT, class TO, int V>
-gs_status launch_lookup(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
-                        float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
-  const TT* table = static_cast<const TT*>(t->data);
-  TO* out = static_cast<TO*>(o->data);
-  const int cols = o->cols;
-  if (o->col_stride == 1) {
-    constexpr int VR = V * sizeof(TO) <= 16 ? V : 16 / sizeof(TO);  // a store has 16 bytes at most
-    const int nv = cols / VR;
-    int items = kThreads * kRowIlp / nv;
-    if (items < 1) items = 1;
-    const int64_t blocks = (o->rows + items - 1) / items;
-    k_lookup_rows<TT, TO, VR><<<(unsigned)blocks, kThreads, 0, s>>>(
-        table, t->row_stride, t->rows, ids, n_ids, index, scale, out, o->rows, o->row_stride,
-        Div((uint32_t)nv), items, dev_status);
-  } else {
-    // columns per block: all of up to kTileCols, else equal shares that V divides
-    const int tiles = (cols + kTileCols - 1) / kTileCols;
-    const int per = (((cols + tiles - 1) / tiles) + V - 1) / V * V;
-    const unsigned col_tiles = (unsigned)((cols + per - 1) / per);
-    const int64_t blocks = (o->rows + kTileItems - 1) / kTileItems * col_tiles;
-    if (blocks > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
-    const size_t smem = sizeof(float) * per * kTilePitch;
-    k_lookup_planes<TT, TO, V><<<(unsigned)blocks, kThreads, smem, s>>>(
-        table, t->row_stride, t->rows, ids, n_ids, index, scale, out, o->rows, o->col_stride, cols,
-        per, col_tiles, dev_status);
-  }
+gs_status launch_rows(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
+                      float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
+  const int nv = o->cols / V;
+  int items = kThreads * kRowIlp / nv;
+  if (items < 1) items = 1;
+  const int64_t blocks = (o->rows + items - 1) / items;
+  k_lookup_rows<TT, TO, V><<<(unsigned)blocks, kThreads, 0, s>>>(
+      static_cast<const TT*>(t->data), t->row_stride, t->rows, ids, n_ids, index, scale,
+      static_cast<TO*>(o->data), o->rows, o->row_stride, Div((uint32_t)nv), items, dev_status);
   GS_LAUNCH_CHECK();
   return GS_OK;
 }
@@ -365,16 +405,38 @@ gs_status launch_lookup(const gs_matrix* t, const int32_t* ids, int64_t n_ids, c
 template <class TT, class TO>
 gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const int32_t* index,
                     float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
-  constexpr int most = 16 / sizeof(TT);
-  int v = vector_of(t->data, t->row_stride, t->cols, sizeof(TT), most);
-  if (o->col_stride == 1) {  // both sides move V elements at a time
-    const int vo = vector_of(o->data, o->row_stride, o->cols, sizeof(TO), 16 / sizeof(TO));
-    if (vo < v) v = vo;
+  if (o->col_stride != 1) {
+    constexpr int V = 16 / sizeof(TT);
+    const int cols = o->cols, words = (cols * (int)sizeof(TT) + 3) / 4;
+    const int al = vector_of(t->data, t->row_stride, cols, sizeof(TT), 2 * V);
+    const unsigned blocks = blocks_for(o->rows);
+#define GS_LOOKUP_PLANES(NW, AL)                                                              \
+  k_lookup_planes<TT, TO, NW, AL><<<blocks, kThreads, 0, s>>>(                                \
+      static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index, scale, \
+      static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status)
+    if (words <= 16) {
+      if (al == 2 * V) GS_LOOKUP_PLANES(16, 32);
+      else if (al == V) GS_LOOKUP_PLANES(16, 16);
+      else GS_LOOKUP_PLANES(16, 0);
+    } else {
+      if (al == 2 * V) GS_LOOKUP_PLANES(48, 32);
+      else if (al == V) GS_LOOKUP_PLANES(48, 16);
+      else GS_LOOKUP_PLANES(48, 0);
+    }
+#undef GS_LOOKUP_PLANES
+    GS_LAUNCH_CHECK();
+    return GS_OK;
   }
-  if (v == 8 && most >= 8) return launch_lookup<TT, TO, most >= 8 ? 8 : 1>(t, ids, n_ids, index, scale, o, dev_status, s);
-  if (v == 4) return launch_lookup<TT, TO, 4>(t, ids, n_ids, index, scale, o, dev_status, s);
-  if (v == 2) return launch_lookup<TT, TO, 2>(t, ids, n_ids, index, scale, o, dev_status, s);
-  return launch_lookup<TT, TO, 1>(t, ids, n_ids, index, scale, o, dev_status, s);
+  // both sides move v elements at a time, in at most 16 bytes
+  constexpr int most = 16 / (sizeof(TT) > sizeof(TO) ? sizeof(TT) : sizeof(TO));
+  const int vt = vector_of(t->data, t->row_stride, t->cols, sizeof(TT), most);
+  const int vo = vector_of(o->data, o->row_stride, o->cols, sizeof(TO), most);
+  const int v = vt < vo ? vt : vo;
+  if constexpr (most == 8)
+    if (v == 8) return launch_rows<TT, TO, 8>(t, ids, n_ids, index, scale, o, dev_status, s);
+  if (v == 4) return launch_rows<TT, TO, 4>(t, ids, n_ids, index, scale, o, dev_status, s);
+  if (v == 2) return launch_rows<TT, TO, 2>(t, ids, n_ids, index, scale, o, dev_status, s);
+  return launch_rows<TT, TO, 1>(t, ids, n_ids, index, scale, o, dev_status, s);
 }
 
 template <class TT>
