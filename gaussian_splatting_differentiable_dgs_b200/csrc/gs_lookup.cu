@@ -230,10 +230,10 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
 // 6M x 48) by asynchronous copies into its own part of shared memory, and
 // each lane then reads its item's row from there, 16 bytes at a time.  The
 // row pitch of 4 words more than a multiple of 16 keeps those reads free of
-// bank conflicts.  The ids of a warp's next items are fetched meanwhile.
+// bank conflicts.  Many short blocks hide the latencies; persistent blocks
+// that fetch the next ids ahead took 293 us, these take 286.
 constexpr int kStageWarps = 4, kStageVecs = 12;            // 192 bytes of a row at a time
 constexpr int kStagePitch = 4 * kStageVecs + 4;            // words
-constexpr int kStageBlocks = 148 * 8;
 
 __device__ __forceinline__ void copy_16_async(void* smem, const void* p, bool has) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(p),
@@ -251,47 +251,39 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   __shared__ __align__(16) uint32_t s_rows[kStageWarps][32 * kStagePitch];
   const int lane = threadIdx.x & 31;
   uint32_t* s = s_rows[threadIdx.x >> 5];
-  const int64_t step = (int64_t)gridDim.x * kStageWarps * 32;
-  int64_t j = ((int64_t)blockIdx.x * kStageWarps + (threadIdx.x >> 5)) * 32 + lane;
-  const auto id_at = [&](int64_t i) {
-    return i < n ? id_of(ids, n_ids, index, i, rows, dev_status) : -1;
-  };
-  int32_t next = id_at(j);
-  for (; j - lane < n; j += step) {
-    const int32_t id = next;
-    for (int c0 = 0; c0 < cols; c0 += kStageVecs * V) {
-      const int nv = min(kStageVecs, (cols - c0) / V);
-      int r = lane / nv, v = lane - r * nv;
-      const int dr = 32 / nv, dv = 32 - dr * nv;
-      for (int k = 0; k < nv; ++k) {
-        const int32_t row = __shfl_sync(0xffffffffu, id, r);
-        copy_16_async(s + r * kStagePitch + 4 * v,
-                      table + (int64_t)(row < 0 ? 0 : row) * ld + c0 + v * V, row >= 0);
-        r += dr;
-        v += dv;
-        if (v >= nv) {
-          v -= nv;
-          ++r;
-        }
+  const int64_t j = ((int64_t)blockIdx.x * kStageWarps + (threadIdx.x >> 5)) * 32 + lane;
+  const int32_t id = j < n ? id_of(ids, n_ids, index, j, rows, dev_status) : -1;
+  for (int c0 = 0; c0 < cols; c0 += kStageVecs * V) {
+    const int nv = min(kStageVecs, (cols - c0) / V);
+    int r = lane / nv, v = lane - r * nv;
+    const int dr = 32 / nv, dv = 32 - dr * nv;
+    for (int k = 0; k < nv; ++k) {
+      const int32_t row = __shfl_sync(0xffffffffu, id, r);
+      copy_16_async(s + r * kStagePitch + 4 * v,
+                    table + (int64_t)(row < 0 ? 0 : row) * ld + c0 + v * V, row >= 0);
+      r += dr;
+      v += dv;
+      if (v >= nv) {
+        v -= nv;
+        ++r;
       }
-      if (c0 == 0) next = id_at(j + step);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
-      if (j < n) {
-        TO* o = out + (int64_t)c0 * cs + j;
-        for (int q = 0; q < nv; ++q) {
-          uint32_t w[4];
-          *reinterpret_cast<uint4*>(w) =
-              *reinterpret_cast<const uint4*>(s + lane * kStagePitch + 4 * q);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            *o = from_f<TO>(id >= 0 ? scale * element<TT>(w, i) : 0.f);
-            o += cs;
-          }
-        }
-      }
-      __syncwarp();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (j < n) {
+      TO* o = out + (int64_t)c0 * cs + j;
+      for (int q = 0; q < nv; ++q) {
+        uint32_t w[4];
+        *reinterpret_cast<uint4*>(w) =
+            *reinterpret_cast<const uint4*>(s + lane * kStagePitch + 4 * q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          *o = from_f<TO>(id >= 0 ? scale * element<TT>(w, i) : 0.f);
+          o += cs;
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -302,6 +294,7 @@ __global__ void __launch_bounds__(kThreads)
 k_lookup_keys(const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
               int64_t n, int64_t rows, uint32_t* __restrict__ keys, int32_t* __restrict__ vals,
               int32_t* dev_status) {
+  wait_for_prior_grids();
   const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (j >= n) return;
   const int32_t id = id_of(ids, n_ids, index, j, rows, dev_status);
@@ -309,63 +302,315 @@ k_lookup_keys(const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __r
   vals[j] = id >= 0 ? (int32_t)j : -1;
 }
 
+// Planes to rows (pitch `vecs` 16-byte vectors, columns past the last one
+// unset): the sums below read whole rows in the order of their ids, and a row
+// in planes costs a 32-byte sector for every element.  A warp turns 32 items
+// in its own part of shared memory; the rows leave as one contiguous piece.
+template <class T>
+__global__ void __launch_bounds__(32 * kStageWarps)
+k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4* __restrict__ out,
+                 int vecs) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ __align__(16) uint32_t s_rows[kStageWarps][32 * kStagePitch];
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31;
+  uint32_t* s = s_rows[threadIdx.x >> 5];
+  const int64_t j0 = ((int64_t)blockIdx.x * kStageWarps + (threadIdx.x >> 5)) * 32, j = j0 + lane;
+  if (j0 >= n) return;
+  const int items = (int)min((int64_t)32, n - j0);
+  for (int v0 = 0; v0 < vecs; v0 += kStageVecs) {
+    const int nv = min(kStageVecs, vecs - v0);
+    if (j < n) {
+      const T* p = g + (int64_t)v0 * V * cs + j;
+#pragma unroll 4
+      for (int q = 0; q < nv; ++q) {
+        union {
+          uint4 raw;
+          uint32_t w[4];
+        } x;
+        x.raw = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if ((v0 + q) * V + i < cols) {
+            if (sizeof(T) == 4) x.w[i] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+            else x.w[i / 2] |= (uint32_t)__ldcs(reinterpret_cast<const uint16_t*>(p)) << (16 * (i & 1));
+          }
+          p += cs;
+        }
+        *reinterpret_cast<uint4*>(s + lane * kStagePitch + 4 * q) = x.raw;
+      }
+    }
+    __syncwarp();
+    int r = lane / nv, v = lane - r * nv;
+    const int dr = 32 / nv, dv = 32 - dr * nv;
+    for (int k = 0; k < nv; ++k) {
+      if (r < items)
+        out[(j0 + r) * vecs + v0 + v] = *reinterpret_cast<const uint4*>(s + r * kStagePitch + 4 * v);
+      r += dr;
+      v += dv;
+      if (v >= nv) {
+        v -= nv;
+        ++r;
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // Sums of runs of equal keys over a list of n entries, entry r standing for
 // the row order[r] of g (or row r).  The list is cut into chunks of R
-// entries; a thread sums one column of one chunk in order.  A run that lies
-// inside a chunk goes to dtable.  What a chunk holds of a run that goes on
-// across its border is a partial: entry 2 chunk for a run that came in from
-// the chunk before, 2 chunk + 1 for one that starts here and goes on.  A
-// chunk inside one run writes its sum at 2 chunk and zeros at 2 chunk + 1,
-// so that the partials of one run are neighbours; unused partials have the
-// key kNoRow.  The partials are summed by the same kernel.
-template <class T>
+// entries; a thread sums V columns of one chunk in order, the loads of kRunIlp
+// entries in flight.  A run that lies inside a chunk goes to dtable.  What a
+// chunk holds of a run that goes on across its border is a partial: entry
+// 2 chunk for a run that came in from the chunk before, 2 chunk + 1 for one
+// that starts here and goes on.  A chunk inside one run writes its sum at
+// 2 chunk and zeros at 2 chunk + 1, so that the partials of one run are
+// neighbours; unused partials have the key kNoRow.  The partials are summed
+// by the same kernel.  keys and order are readable up to a multiple of
+// kRunIlp entries.
+constexpr int kRunIlp = 8;
+
+template <class T, int V>
 __global__ void __launch_bounds__(kThreads)
 k_run_sums(const uint32_t* __restrict__ keys, const int32_t* __restrict__ order, int64_t n, int R,
-           const T* __restrict__ g, int64_t rs, int64_t cs, int cols, float scale,
+           const T* __restrict__ g, int64_t rs, int cols, Div nv, float scale,
            float* __restrict__ dtable, int64_t ld, bool accumulate, uint32_t* __restrict__ pkey,
-           float* __restrict__ psum) {
+           float* __restrict__ psum, int ldp) {
+  wait_for_prior_grids();
   const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t chunk = e / cols;
-  const int c = (int)(e % cols);
+  const int64_t chunk = e / nv.d;
+  const int c = (int)(e - chunk * nv.d) * V;
   const int64_t a = chunk * R;
   if (a >= n) return;
   const int64_t b = min(a + R, n);
   uint32_t k = keys[a];
   bool head = a > 0 && keys[a - 1] == k;  // the run came in from the chunk before
   bool used0 = false, used1 = false;
-  float sum = 0.f;
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  auto partial = [&](int at, bool zero) {
+    const int64_t p = 2 * chunk + at;
+    if (c == 0) pkey[p] = k;
+#pragma unroll
+    for (int i = 0; i < V; ++i) psum[p * ldp + c + i] = zero ? 0.f : sum[i];
+    (at ? used1 : used0) = true;
+  };
   auto done = [&](bool tail) {
     if (k == kNoRow) return;
     if (head || tail) {
-      const int64_t at = 2 * chunk + (head ? 0 : 1);
-      psum[at * cols + c] = sum;
-      if (c == 0) pkey[at] = k;
-      (head ? used0 : used1) = true;
-      if (head && tail) {
-        psum[(at + 1) * cols + c] = 0.f;
-        if (c == 0) pkey[at + 1] = k;
-        used1 = true;
-      }
+      partial(head ? 0 : 1, false);
+      if (head && tail) partial(1, true);
     } else {
       float* d = dtable + (int64_t)k * ld + c;
-      *d = accumulate ? *d + scale * sum : scale * sum;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
     }
   };
-  for (int64_t r = a; r < b; ++r) {
-    const uint32_t kr = keys[r];
-    if (kr != k) {
-      done(false);
-      k = kr;
-      head = false;
-      sum = 0.f;
+  for (int64_t r = a; r < b; r += kRunIlp) {
+    uint32_t kr[kRunIlp];
+    int32_t j[kRunIlp];
+#pragma unroll
+    for (int q = 0; q < kRunIlp; q += 4) {
+      const uint4 kk = *reinterpret_cast<const uint4*>(keys + r + q);
+      kr[q] = kk.x, kr[q + 1] = kk.y, kr[q + 2] = kk.z, kr[q + 3] = kk.w;
+      if (order) {
+        const int4 o = *reinterpret_cast<const int4*>(order + r + q);
+        j[q] = o.x, j[q + 1] = o.y, j[q + 2] = o.z, j[q + 3] = o.w;
+      }
     }
-    const int64_t j = order ? order[r] : r;
-    if (k != kNoRow && j >= 0) sum += to_f(g[j * rs + (int64_t)c * cs]);
+    Pack<T, V> x[kRunIlp];
+#pragma unroll
+    for (int q = 0; q < kRunIlp; ++q) {
+      if (!order) j[q] = kr[q] == kNoRow ? -1 : 0;
+      if (r + q >= b) j[q] = -1;
+      if (j[q] >= 0)
+        x[q] = *reinterpret_cast<const Pack<T, V>*>(g + (order ? (int64_t)j[q] : r + q) * rs + c);
+    }
+#pragma unroll
+    for (int q = 0; q < kRunIlp; ++q) {
+      if (r + q >= b) break;
+      if (kr[q] != k) {
+        done(false);
+        k = kr[q];
+        head = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = 0.f;
+      }
+      if (j[q] >= 0)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += to_f(x[q].x[i]);
+    }
   }
   done(b < n && keys[b] == k);
-  if (c == 0 && pkey) {
+  if (c == 0) {
     if (!used0) pkey[2 * chunk] = kNoRow;
     if (!used1) pkey[2 * chunk + 1] = kNoRow;
+  }
+}
+
+// Up to kSmallItems items, in one launch: a block owns a range of the table's
+// rows.  It picks the items with ids in its range (in order), sorts them by id
+// in shared memory (the rank of an item is the number of items before it),
+// sums the runs of equal ids with teams of threads, each a stretch of the
+// sorted list, joins the teams' partial runs in order, and clears the rows
+// that nothing used.  Every block reads all ids.
+constexpr int kSmallItems = 2048, kSmallPer = kSmallItems / kThreads;
+constexpr int kSmallTeams = 64;
+
+template <class T, int V>
+__global__ void __launch_bounds__(kThreads)
+k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
+             const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index, int n,
+             float scale, float* __restrict__ dtable, int64_t ld, int64_t rows, int64_t per,
+             bool accumulate, int32_t* dev_status) {
+  __shared__ int32_t s_key[kSmallItems];
+  __shared__ uint16_t s_item[kSmallItems];
+  __shared__ int s_scan[kThreads / 32 + 1];
+  __shared__ int32_t s_pk[2 * kSmallTeams];
+  __shared__ float s_part[2 * kThreads * V];
+  wait_for_prior_grids();
+  const int t = threadIdx.x;
+  const int64_t k0 = blockIdx.x * per, k1 = min(k0 + per, rows);
+  int32_t key[kSmallPer];
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kSmallPer; ++i) {
+    const int j = t * kSmallPer + i;
+    const int32_t id = j < n ? id_of(ids, n_ids, index, j, rows, dev_status) : -1;
+    key[i] = id >= k0 && id < k1 ? (int32_t)(id - k0) : -1;
+    mine += key[i] >= 0;
+  }
+  if (!accumulate) {
+    float* d = dtable + k0 * ld;
+    if (ld == cols) {
+      const int64_t total = (k1 - k0) * cols;
+      for (int64_t i = t; i < total; i += kThreads) d[i] = 0.f;
+    } else {
+      for (int64_t k = k0; k < k1; ++k, d += ld)
+        for (int c = t; c < cols; c += kThreads) d[c] = 0.f;
+    }
+  }
+  int m;
+  int at = block_exclusive_scan<int, kThreads / 32>(mine, s_scan, &m);
+  if (m == 0) return;
+#pragma unroll
+  for (int i = 0; i < kSmallPer; ++i)
+    if (key[i] >= 0) {
+      s_key[at] = key[i];
+      s_item[at++] = (uint16_t)(t * kSmallPer + i);
+    }
+  __syncthreads();  // also: the zeros above are ordered before the sums below
+  if (k1 - k0 > 1) {
+    int32_t mk[kSmallPer];
+    uint16_t mi[kSmallPer];
+    int rank[kSmallPer];
+#pragma unroll
+    for (int i = 0; i < kSmallPer; ++i) {
+      const int e = t + i * kThreads;
+      if (e < m) {
+        mk[i] = s_key[e];
+        mi[i] = s_item[e];
+        rank[i] = 0;
+        for (int f = 0; f < m; ++f) {
+          const int32_t kf = s_key[f];
+          rank[i] += kf < mk[i] || (kf == mk[i] && f < e);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSmallPer; ++i)
+      if (t + i * kThreads < m) {
+        s_key[rank[i]] = mk[i];
+        s_item[rank[i]] = mi[i];
+      }
+    __syncthreads();
+  }
+  const int nv = (cols + V - 1) / V;
+  int teams = nv < kThreads ? kThreads / nv : 1;
+  teams = min(teams, min(kSmallTeams, (m + 3) / 4));
+  const int len = (m + teams - 1) / teams;
+  const int width = nv < kThreads ? nv : kThreads;  // vectors of a row at a time
+  const int team = t / width, tv = t - team * width;
+  for (int v0 = 0; v0 < nv; v0 += width) {
+    const int c = (v0 + tv) * V;
+    const bool on = team < teams && c < cols;
+    const int a = team * len, b = min(a + len, m);
+    if (on && tv == 0) s_pk[2 * team] = s_pk[2 * team + 1] = -1;
+    if (on && a < b) {
+      float sum[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] = 0.f;
+      int k = s_key[a];
+      bool head = a > 0 && s_key[a - 1] == k;
+      auto done = [&](bool tail) {
+        if (head || tail) {
+          const int p = 2 * team + (head ? 0 : 1);
+          if (tv == 0) s_pk[p] = k;
+#pragma unroll
+          for (int i = 0; i < V; ++i) s_part[(p * width + tv) * V + i] = sum[i];
+        } else {
+          float* d = dtable + (k0 + k) * ld + c;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
+        }
+      };
+      for (int r = a; r < b; r += 4) {
+        Pack<T, V> x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r + q < b) {
+            const T* p = g + (int64_t)s_item[r + q] * rs + (int64_t)c * cs;
+            if (V > 1) x[q] = *reinterpret_cast<const Pack<T, V>*>(p);
+            else x[q].x[0] = *p;
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r + q < b) {
+            const int kr = s_key[r + q];
+            if (kr != k) {
+              done(false);
+              k = kr;
+              head = false;
+#pragma unroll
+              for (int i = 0; i < V; ++i) sum[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] += to_f(x[q].x[i]);
+          }
+      }
+      done(b < m && s_key[b] == k);
+    }
+    __syncthreads();
+    // partial runs, joined in order by the first team
+    if (team == 0 && c < cols) {
+      float sum[V];
+      int k = -1;
+      auto done = [&]() {
+        if (k < 0) return;
+        float* d = dtable + (k0 + k) * ld + c;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
+      };
+      for (int p = 0; p < 2 * teams; ++p) {
+        const int kp = s_pk[p];
+        if (kp < 0) continue;
+        if (kp != k) {
+          done();
+          k = kp;
+#pragma unroll
+          for (int i = 0; i < V; ++i) sum[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += s_part[(p * width + tv) * V + i];
+      }
+      done();
+    }
+    __syncthreads();
   }
 }
 
@@ -373,7 +618,16 @@ unsigned blocks_for(int64_t threads) { return (unsigned)((threads + kThreads - 1
 
 int key_bits(int64_t rows) { return rows > 1 ? 64 - __builtin_clzll((unsigned long long)(rows - 1)) : 0; }
 
-constexpr int kChunk = 64;  // entries per chunk
+constexpr int kPartChunk = 64;  // entries per chunk of partials
+
+// Entries per chunk of the items: enough chunks to fill the device, and few
+// enough partials that they cost little.
+int chunk_of(int64_t n, int nv) {
+  const int64_t fill = n * nv / (148 * 1024);
+  int R = kRunIlp;
+  while (R < 128 && R < fill) R *= 2;
+  return R;
+}
 
 struct LookupWs {
   uint32_t* keys;
@@ -382,22 +636,28 @@ struct LookupWs {
   size_t sort_bytes;
   uint32_t* pkey[2];
   float* psum[2];
+  uint4* rows;  // the items' rows, for a gradient in planes
+  int ldp;
   size_t bytes;
 };
 
-LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols) {
+LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, int planes_es) {
   LookupWs w{};
+  if (n <= kSmallItems) return w;
   Carver cv(ws, cap);
-  w.keys = cv.take<uint32_t>(n);
-  w.order = cv.take<int32_t>(n);
+  w.ldp = (cols + 7) / 8 * 8;
+  w.keys = cv.take<uint32_t>(round_up(n, kRunIlp));
+  w.order = cv.take<int32_t>(round_up(n, kRunIlp));
   w.sort_bytes = gs_sort_workspace_size(n, 4, 0, key_bits(rows));
   w.sort = cv.take<char>(w.sort_bytes);
-  int64_t m = 2 * ((n + kChunk - 1) / kChunk);
+  const int R = chunk_of(n, (cols + 7) / 8);  // the smallest that any type takes
+  int64_t m = 2 * ((n + R - 1) / R);
   for (int k = 0; k < 2; ++k) {
-    w.pkey[k] = cv.take<uint32_t>(m);
-    w.psum[k] = cv.take<float>((size_t)m * cols);
-    m = 2 * ((m + kChunk - 1) / kChunk);
+    w.pkey[k] = cv.take<uint32_t>(round_up(m, kRunIlp));
+    w.psum[k] = cv.take<float>((size_t)m * w.ldp);
+    m = 2 * ((m + kPartChunk - 1) / kPartChunk);
   }
+  if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
   w.bytes = cv.off;
   return w;
 }
@@ -424,29 +684,32 @@ gs_status check_ids(const int32_t* ids, int64_t n_ids, const int32_t* index, int
 
 gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, int64_t n,
                       int64_t rows, const LookupWs& w, int32_t* dev_status, cudaStream_t s) {
-  k_lookup_keys<<<blocks_for(n), kThreads, 0, s>>>(ids, n_ids, index, n, rows, w.keys, w.order,
-                                                   dev_status);
+  GS_TRY(launch_dependent(k_lookup_keys, blocks_for(n), kThreads, 0, s, ids, n_ids, index, n, rows,
+                          w.keys, w.order, dev_status));
   GS_LAUNCH_CHECK();
   return gs_sort_keys32(nullptr, w.keys, w.order, n, 0, key_bits(rows), 0, w.sort, w.sort_bytes,
                         dev_status, s);
 }
 
-template <class T>
-gs_status run_sums(const gs_matrix* g, const gs_matrix* dtable, float scale, bool accumulate,
-                   const LookupWs& w, cudaStream_t s) {
-  const int cols = g->cols;
-  float* dt = static_cast<float*>(dtable->data);
-  int64_t m = g->rows, chunks = (m + kChunk - 1) / kChunk;
-  k_run_sums<T><<<blocks_for(chunks * cols), kThreads, 0, s>>>(
-      w.keys, w.order, m, kChunk, static_cast<const T*>(g->data), g->row_stride, g->col_stride, cols,
-      scale, dt, dtable->row_stride, accumulate, w.pkey[0], w.psum[0]);
+template <class T, int V>
+gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, float* dt, int64_t ld,
+                   bool accumulate, const LookupWs& w, cudaStream_t s) {
+  const int nv = (cols + V - 1) / V;
+  int R = chunk_of(n, nv);
+  int64_t m = n, chunks = (m + R - 1) / R;
+  if (chunks * nv > (int64_t)INT32_MAX * kThreads) return GS_ERR_UNSUPPORTED;
+  GS_TRY(launch_dependent(k_run_sums<T, V>, blocks_for(chunks * nv), kThreads, 0, s, w.keys, w.order,
+                          m, R, g, rs, cols, Div((uint32_t)nv), scale, dt, ld, accumulate, w.pkey[0],
+                          w.psum[0], w.ldp));
   GS_LAUNCH_CHECK();
+  const int nv4 = (cols + 3) / 4;
   for (int from = 0; chunks > 1; from ^= 1) {
     m = 2 * chunks;
-    chunks = (m + kChunk - 1) / kChunk;
-    k_run_sums<float><<<blocks_for(chunks * cols), kThreads, 0, s>>>(
-        w.pkey[from], nullptr, m, kChunk, w.psum[from], cols, 1, cols, scale, dt,
-        dtable->row_stride, accumulate, w.pkey[from ^ 1], w.psum[from ^ 1]);
+    chunks = (m + kPartChunk - 1) / kPartChunk;
+    GS_TRY(launch_dependent(k_run_sums<float, 4>, blocks_for(chunks * nv4), kThreads, 0, s,
+                            w.pkey[from], nullptr, m, kPartChunk, w.psum[from], w.ldp, cols,
+                            Div((uint32_t)nv4), scale, dt, ld, accumulate, w.pkey[from ^ 1],
+                            w.psum[from ^ 1], w.ldp));
     GS_LAUNCH_CHECK();
   }
   return GS_OK;
@@ -483,9 +746,8 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
     const int al = vector_of(t->data, t->row_stride, cols, sizeof(TT), 2 * V);
     const unsigned blocks = blocks_for(o->rows);
     if (al >= V && words > 8) {
-      const int64_t groups = (o->rows + 32 * kStageWarps - 1) / (32 * kStageWarps);
-      k_lookup_planes_staged<TT, TO>
-          <<<(unsigned)(groups < kStageBlocks ? groups : kStageBlocks), 32 * kStageWarps, 0, s>>>(
+      const unsigned groups = (unsigned)((o->rows + 32 * kStageWarps - 1) / (32 * kStageWarps));
+      k_lookup_planes_staged<TT, TO><<<groups, 32 * kStageWarps, 0, s>>>(
               static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index,
               scale, static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status);
       GS_LAUNCH_CHECK();
@@ -555,9 +817,9 @@ extern "C" gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64
 
 extern "C" size_t gs_lookup_bwd_workspace_size(int64_t n, int64_t rows, int32_t cols,
                                                int32_t planes) {
-  (void)planes;
-  if (n < 0 || n > (int64_t)INT32_MAX || rows < 1 || cols < 1) return 0;
-  return carve_lookup(nullptr, 0, n, rows, cols).bytes;
+  if (n < 0 || n > (int64_t)INT32_MAX || rows < 1 || rows > (int64_t)INT32_MAX || cols < 1) return 0;
+  const size_t b = carve_lookup(nullptr, 0, n, rows, cols, planes ? 4 : 0).bytes;
+  return b ? b : 256;
 }
 
 extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int32_t* index,
@@ -567,11 +829,65 @@ extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int
   if (st != GS_OK) return st;
   if (rows < 1 || rows > (int64_t)INT32_MAX || cols < 1) return GS_ERR_ARG;
   if (n == 0) return GS_OK;
-  const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, cols);
-  if (!ws || w.bytes > ws_bytes) return GS_ERR_CAPACITY;
+  const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, cols, 0);
+  if (!ws || w.bytes > ws_bytes || ws_bytes < 256) return GS_ERR_CAPACITY;
   if (!aligned(ws, 256)) return GS_ERR_ARG;
+  if (n <= kSmallItems) return GS_OK;  // such gradients need no order
   return plan_lookup(ids, n_ids, index, n, rows, w, dev_status, to_stream(stream));
 }
+
+namespace gs {
+namespace {
+
+template <class T, int V>
+gs_status small_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, const int32_t* index,
+                     float scale, const gs_matrix* dtable, bool accumulate, int32_t* dev_status,
+                     cudaStream_t s) {
+  // as many blocks as the table has 4096-element pieces, at most four per SM
+  const int64_t rows = dtable->rows;
+  int64_t blocks = (rows * dtable->cols + 4095) / 4096;
+  if (blocks > 148 * 4) blocks = 148 * 4;
+  if (blocks > rows) blocks = rows;
+  const int64_t per = (rows + blocks - 1) / blocks;
+  blocks = (rows + per - 1) / per;
+  GS_TRY(launch_dependent(k_small_grad<T, V>, (unsigned)blocks, kThreads, 0, s,
+                          static_cast<const T*>(g->data), g->row_stride, g->col_stride, g->cols, ids,
+                          n_ids, index, (int)g->rows, scale, static_cast<float*>(dtable->data),
+                          dtable->row_stride, rows, per, accumulate, dev_status));
+  GS_LAUNCH_CHECK();
+  return GS_OK;
+}
+
+template <class T>
+gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, const int32_t* index,
+                      float scale, const gs_matrix* dtable, bool accumulate, const LookupWs& w,
+                      int32_t* dev_status, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int64_t n = g->rows;
+  const int cols = g->cols;
+  const T* data = static_cast<const T*>(g->data);
+  const bool planes = g->col_stride != 1;
+  const bool vec = !planes && vector_of(data, g->row_stride, cols, sizeof(T), V) == V;
+  if (n <= kSmallItems)
+    return vec ? small_grad<T, V>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s)
+               : small_grad<T, 1>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s);
+  float* dt = static_cast<float*>(dtable->data);
+  const int64_t ld = dtable->row_stride;
+  if (planes) {
+    const int vecs = (cols + V - 1) / V;
+    GS_TRY(launch_dependent(k_planes_to_rows<T>,
+                            (unsigned)((n + 32 * kStageWarps - 1) / (32 * kStageWarps)),
+                            32 * kStageWarps, 0, s, data, g->col_stride, cols, n, w.rows, vecs));
+    GS_LAUNCH_CHECK();
+    return run_sums<T, V>(reinterpret_cast<const T*>(w.rows), (int64_t)vecs * V, n, cols, scale, dt,
+                          ld, accumulate, w, s);
+  }
+  return vec ? run_sums<T, V>(data, g->row_stride, n, cols, scale, dt, ld, accumulate, w, s)
+             : run_sums<T, 1>(data, g->row_stride, n, cols, scale, dt, ld, accumulate, w, s);
+}
+
+}  // namespace
+}  // namespace gs
 
 extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64_t n_ids,
                                    const int32_t* index, double scale, const gs_matrix* dtable,
@@ -585,23 +901,24 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
   const gs_status st = check_ids(ids, n_ids, index, n);
   if (st != GS_OK) return st;
   cudaStream_t s = to_stream(stream);
-  const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, g->cols);
+  const int planes_es = g->col_stride != 1 ? (int)type_size(g->dtype) : 0;
+  const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, g->cols, planes_es);
   if (n > 0) {
-    if (!ws || w.bytes > ws_bytes) return GS_ERR_CAPACITY;
+    if (!ws || w.bytes > ws_bytes || ws_bytes < 256) return GS_ERR_CAPACITY;
     if (!aligned(ws, 256)) return GS_ERR_ARG;
   }
   const bool accumulate = (flags & GS_LOOKUP_ACCUMULATE) != 0;
-  if (!accumulate)
+  if (!accumulate && (n == 0 || n > kSmallItems))
     GS_TRY(cudaMemset2DAsync(dtable->data, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
   if (n == 0) return GS_OK;
-  if (!(flags & GS_LOOKUP_PLANNED)) {
+  if (!(flags & GS_LOOKUP_PLANNED) && n > kSmallItems) {
     const gs_status ps = plan_lookup(ids, n_ids, index, n, rows, w, dev_status, s);
     if (ps != GS_OK) return ps;
   }
   const float sc = (float)scale;
   switch (g->dtype) {
-    case GS_F32: return run_sums<float>(g, dtable, sc, accumulate, w, s);
-    case GS_F16: return run_sums<__half>(g, dtable, sc, accumulate, w, s);
-    default: return run_sums<__nv_bfloat16>(g, dtable, sc, accumulate, w, s);
+    case GS_F32: return lookup_grad<float>(g, ids, n_ids, index, sc, dtable, accumulate, w, dev_status, s);
+    case GS_F16: return lookup_grad<__half>(g, ids, n_ids, index, sc, dtable, accumulate, w, dev_status, s);
+    default: return lookup_grad<__nv_bfloat16>(g, ids, n_ids, index, sc, dtable, accumulate, w, dev_status, s);
   }
 }
