@@ -287,19 +287,159 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   }
 }
 
-// Sort keys and values of the gradient's items: key = id, value = j.  An
-// item without a row takes the last key and a negative value, which adds
-// nothing, so that the keys need no bit more than the rows do.
+// Stable radix sort of the gradient's items by id: pairs (id, item), digits
+// of up to 10 bits, most often one or two passes.  A pass counts the digits
+// of each tile of kSortTile items, scans the counts along the tiles, and
+// scatters.  The first pass reads the ids themselves.  An item without a row
+// takes the last id and item -1, which adds nothing, so that the keys need no
+// bit more than the rows do.  Against the library's general 32-bit sort (8
+// bits per pass, an even number of passes, a histogram before them, tiles of
+// 4096) 2.5M items over 2^16 rows take half the time.
+constexpr int kSortItems = 8, kSortTile = kThreads * kSortItems, kMaxDigit = 10;
+
+struct Ids {
+  const int32_t* ids;
+  const int32_t* index;
+  int64_t n_ids, rows;
+};
+
+__device__ __forceinline__ uint2 pair_of(const Ids& s, int64_t j, int32_t* dev_status) {
+  const int32_t id = id_of(s.ids, s.n_ids, s.index, j, s.rows, dev_status);
+  return id >= 0 ? make_uint2((uint32_t)id, (uint32_t)j)
+                 : make_uint2((uint32_t)(s.rows - 1), 0xffffffffu);
+}
+
+// counts[digit][tile]; the first pass also clears `zeros` floats of dtable
+template <bool FIRST>
 __global__ void __launch_bounds__(kThreads)
-k_lookup_keys(const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
-              int64_t n, int64_t rows, uint32_t* __restrict__ keys, int32_t* __restrict__ vals,
-              int32_t* dev_status) {
+k_sort_count(const __grid_constant__ Ids src, const uint2* __restrict__ pairs, int64_t n, int shift,
+             int bits, uint32_t* __restrict__ counts, float* __restrict__ dtable, int64_t zeros,
+             int32_t* dev_status) {
+  __shared__ uint32_t s_hist[1 << kMaxDigit];
   wait_for_prior_grids();
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= n) return;
-  const int32_t id = id_of(ids, n_ids, index, j, rows, dev_status);
-  keys[j] = id >= 0 ? (uint32_t)id : (uint32_t)(rows - 1);
-  vals[j] = id >= 0 ? (int32_t)j : -1;
+  const int t = threadIdx.x, bins = 1 << bits;
+  for (int d = t; d < bins; d += kThreads) s_hist[d] = 0;
+  __syncthreads();
+  const int64_t j0 = (int64_t)blockIdx.x * kSortTile + t;
+  uint32_t key[kSortItems];
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const int64_t j = j0 + i * kThreads;
+    if (j < n) key[i] = FIRST ? pair_of(src, j, dev_status).x : pairs[j].x;
+  }
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i)
+    if (j0 + i * kThreads < n) atomicAdd(&s_hist[(key[i] >> shift) & (bins - 1)], 1u);
+  if (FIRST)
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < zeros; i += (int64_t)gridDim.x * kThreads)
+      dtable[i] = 0.f;
+  __syncthreads();
+  for (int d = t; d < bins; d += kThreads) counts[(int64_t)d * gridDim.x + blockIdx.x] = s_hist[d];
+}
+
+// counts of digit blockIdx.x -> exclusive sums over the tiles; total[digit]
+__global__ void __launch_bounds__(kThreads)
+k_sort_scan(uint32_t* __restrict__ counts, int64_t tiles, uint32_t* __restrict__ total) {
+  __shared__ uint32_t s_scan[kThreads / 32 + 1];
+  wait_for_prior_grids();
+  uint32_t* c = counts + (int64_t)blockIdx.x * tiles;
+  uint32_t base = 0;
+  for (int64_t i0 = 0; i0 < tiles; i0 += kThreads * 4) {
+    const int64_t i = i0 + threadIdx.x * 4;
+    uint32_t v[4], sum = 0, all;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = i + k < tiles ? c[i + k] : 0;
+      sum += v[k];
+    }
+    uint32_t at = base + block_exclusive_scan<uint32_t, kThreads / 32>(sum, s_scan, &all);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < tiles) {
+        c[i + k] = at;
+        at += v[k];
+      }
+    base += all;
+  }
+  if (threadIdx.x == 0) total[blockIdx.x] = base;
+}
+
+size_t scatter_smem(int bits) {
+  return sizeof(uint2) * kSortTile + ((size_t)1 << bits) * (2 * sizeof(uint32_t) + 2 * (kThreads / 32));
+}
+
+template <bool FIRST>
+__global__ void __launch_bounds__(kThreads)
+k_sort_scatter(const __grid_constant__ Ids src, const uint2* __restrict__ pairs, int64_t n, int shift,
+               int bits, const uint32_t* __restrict__ counts, const uint32_t* __restrict__ total,
+               uint2* __restrict__ out) {
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  __shared__ uint32_t s_scan[kThreads / 32 + 1];
+  const int bins = 1 << bits;
+  uint2* s_pair = reinterpret_cast<uint2*>(s_raw);
+  uint32_t* s_loc = reinterpret_cast<uint32_t*>(s_pair + kSortTile);  // digit's start in the tile
+  uint32_t* s_base = s_loc + bins;                                    // ... in the output, less that
+  uint16_t* s_hist = reinterpret_cast<uint16_t*>(s_base + bins);      // [warp][digit]
+  wait_for_prior_grids();
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  for (int i = t; i < bins * (kThreads / 32) / 2; i += kThreads) reinterpret_cast<uint32_t*>(s_hist)[i] = 0;
+  const int64_t j0 = (int64_t)blockIdx.x * kSortTile;
+  const int items = (int)min((int64_t)kSortTile, n - j0);
+  uint2 p[kSortItems];
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {  // a warp's items are neighbours
+    const int e = w * 32 * kSortItems + i * 32 + lane;
+    if (e < items) p[i] = FIRST ? pair_of(src, j0 + e, nullptr) : pairs[j0 + e];
+    else p[i] = make_uint2(0xffffffffu, 0);  // behind the last item: behind all of the last digit
+  }
+  __syncthreads();
+  // rank of an item among its warp's items with the same digit
+  int rank[kSortItems];
+  uint16_t* hist = s_hist + w * bins;
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const uint32_t d = (p[i].x >> shift) & (bins - 1);
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int before = __popc(same & ((1u << lane) - 1)), had = hist[d];
+    rank[i] = had + before;
+    __syncwarp();
+    if (before == 0) hist[d] = (uint16_t)(had + __popc(same));
+    __syncwarp();
+  }
+  __syncthreads();
+  // digits' starts: thread t has `per` neighbouring digits
+  const int per = (bins + kThreads - 1) / kThreads;
+  uint32_t local = 0, global = 0;
+  for (int d = t * per; d < min(bins, (t + 1) * per); ++d) {
+    uint32_t run = 0;
+    for (int k = 0; k < kThreads / 32; ++k) {
+      const uint32_t c = s_hist[k * bins + d];
+      s_hist[k * bins + d] = (uint16_t)run;
+      run += c;
+    }
+    s_loc[d] = local;
+    s_base[d] = global;
+    local += run;
+    global += total[d];
+  }
+  uint32_t all;
+  const uint32_t local0 = block_exclusive_scan<uint32_t, kThreads / 32>(local, s_scan, &all);
+  const uint32_t global0 = block_exclusive_scan<uint32_t, kThreads / 32>(global, s_scan, &all);
+  for (int d = t * per; d < min(bins, (t + 1) * per); ++d) {
+    s_loc[d] += local0;
+    s_base[d] += global0 + counts[(int64_t)d * gridDim.x + blockIdx.x] - s_loc[d];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const uint32_t d = (p[i].x >> shift) & (bins - 1);
+    s_pair[s_loc[d] + hist[d] + rank[i]] = p[i];
+  }
+  __syncthreads();
+  for (int i = t; i < items; i += kThreads) {
+    const uint2 x = s_pair[i];
+    out[s_base[(x.x >> shift) & (bins - 1)] + i] = x;
+  }
 }
 
 // Planes to rows (pitch `vecs` 16-byte vectors, columns past the last one
@@ -357,96 +497,169 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
   }
 }
 
-// Sums of runs of equal keys over a list of n entries, entry r standing for
-// the row order[r] of g (or row r).  The list is cut into chunks of R
-// entries; a thread sums V columns of one chunk in order, the loads of kRunIlp
-// entries in flight.  A run that lies inside a chunk goes to dtable.  What a
-// chunk holds of a run that goes on across its border is a partial: entry
-// 2 chunk for a run that came in from the chunk before, 2 chunk + 1 for one
-// that starts here and goes on.  A chunk inside one run writes its sum at
-// 2 chunk and zeros at 2 chunk + 1, so that the partials of one run are
-// neighbours; unused partials have the key kNoRow.  The partials are summed
-// by the same kernel.  keys and order are readable up to a multiple of
-// kRunIlp entries.
-constexpr int kRunIlp = 8;
+// Sums of runs of equal keys over a list of n entries: the sorted items
+// (FIRST: pairs of a key and a row of g) or partials (keys, entry r being row
+// r).  A block takes a stretch of the list, a team of `width` threads (V
+// columns each) `len` entries of it, kRunIlp rows in flight.  A run inside a
+// team's entries goes to dtable.  What a team holds of a run that crosses its
+// borders goes to shared memory: slot 0 if the run came in from before, else
+// slot 1; the team in which a run starts then adds the following teams' slots
+// 0 in order.  Runs that cross the block's borders leave as partials: entry
+// 2 block for a run that came in, 2 block + 1 for one that starts here and
+// goes on; a block inside one run writes its sum at 2 block and zeros at
+// 2 block + 1, so that a run's partials are neighbours.  Unused partials have
+// the key kNoRow.  The same kernel sums the partials until one block is left.
+// Lists are readable up to a multiple of kRunIlp entries.
+constexpr int kRunIlp = 8, kMaxTeams = 64;
 
-template <class T, int V>
+struct RunShape {
+  int width, teams, threads, len, col_tiles;
+  int64_t blocks;
+  RunShape(int64_t n, int cols, int V, int len0) : len(len0) {
+    const int nv = (cols + V - 1) / V;
+    width = nv < kThreads ? nv : kThreads;
+    teams = kThreads / width < kMaxTeams ? kThreads / width : kMaxTeams;
+    threads = (teams * width + 31) / 32 * 32;
+    col_tiles = (nv + width - 1) / width;
+    // long stretches while they leave eight blocks for each SM
+    if (!len)
+      for (len = kRunIlp; len < 64 && n / (2 * len * teams) >= 148 * 8; len *= 2) {
+      }
+    blocks = (n + (int64_t)len * teams - 1) / ((int64_t)len * teams);
+  }
+};
+
+template <class T, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
-k_run_sums(const uint32_t* __restrict__ keys, const int32_t* __restrict__ order, int64_t n, int R,
-           const T* __restrict__ g, int64_t rs, int cols, Div nv, float scale,
-           float* __restrict__ dtable, int64_t ld, bool accumulate, uint32_t* __restrict__ pkey,
-           float* __restrict__ psum, int ldp) {
+k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, int64_t n, int len,
+           int teams, int width, int col_tiles, const T* __restrict__ g, int64_t rs, int cols,
+           float scale, float* __restrict__ dtable, int64_t ld, bool accumulate,
+           uint32_t* __restrict__ pkey, float* __restrict__ psum, int ldp) {
+  __shared__ __align__(16) float s_part[2][kThreads * V];
+  __shared__ bool s_start[kMaxTeams], s_whole[kMaxTeams];
   wait_for_prior_grids();
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t chunk = e / nv.d;
-  const int c = (int)(e - chunk * nv.d) * V;
-  const int64_t a = chunk * R;
-  if (a >= n) return;
-  const int64_t b = min(a + R, n);
-  uint32_t k = keys[a];
-  bool head = a > 0 && keys[a - 1] == k;  // the run came in from the chunk before
-  bool used0 = false, used1 = false;
+  const int t = threadIdx.x, team = t / width, tv = t - team * width;
+  const int64_t blk = blockIdx.x / col_tiles;
+  const int c = ((int)(blockIdx.x % col_tiles) * width + tv) * V;
+  const int64_t A = blk * teams * len, B = min(A + (int64_t)teams * len, n);
+  const int used = (int)((B - A + len - 1) / len);  // teams with entries
+  const int64_t a = A + (int64_t)team * len, b = min(a + len, B);
+  const bool on = team < used && c < cols;
+  const auto key_at = [&](int64_t r) { return FIRST ? pairs[r].x : keys[r]; };
+  uint32_t k = kNoRow;
+  bool head = false, start = false, whole = false;
   float sum[V];
+  const auto to_table = [&](uint32_t key) {
+    float* d = dtable + (int64_t)key * ld + c;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum[i] = 0.f;
-  auto partial = [&](int at, bool zero) {
-    const int64_t p = 2 * chunk + at;
-    if (c == 0) pkey[p] = k;
-#pragma unroll
-    for (int i = 0; i < V; ++i) psum[p * ldp + c + i] = zero ? 0.f : sum[i];
-    (at ? used1 : used0) = true;
+    for (int i = 0; i < V; ++i)
+      if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
   };
-  auto done = [&](bool tail) {
+  const auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  };
+  const auto done = [&](bool tail) {
     if (k == kNoRow) return;
-    if (head || tail) {
-      partial(head ? 0 : 1, false);
-      if (head && tail) partial(1, true);
-    } else {
-      float* d = dtable + (int64_t)k * ld + c;
+    if (!head && !tail) return to_table(k);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
-    }
+    for (int i = 0; i < V; ++i) s_part[head ? 0 : 1][t * V + i] = sum[i];
+    start = !head;
+    whole = head && tail;
   };
-  for (int64_t r = a; r < b; r += kRunIlp) {
-    uint32_t kr[kRunIlp];
-    int32_t j[kRunIlp];
+  if (on) {
+    k = key_at(a);
+    head = a > 0 && key_at(a - 1) == k && k != kNoRow;
+    clear();
+    for (int64_t r = a; r < b; r += kRunIlp) {
+      uint32_t kr[kRunIlp];
+      int32_t j[kRunIlp];
 #pragma unroll
-    for (int q = 0; q < kRunIlp; q += 4) {
-      const uint4 kk = *reinterpret_cast<const uint4*>(keys + r + q);
-      kr[q] = kk.x, kr[q + 1] = kk.y, kr[q + 2] = kk.z, kr[q + 3] = kk.w;
-      if (order) {
-        const int4 o = *reinterpret_cast<const int4*>(order + r + q);
-        j[q] = o.x, j[q + 1] = o.y, j[q + 2] = o.z, j[q + 3] = o.w;
+      for (int q = 0; q < kRunIlp; q += FIRST ? 2 : 4) {
+        const uint4 x = FIRST ? *reinterpret_cast<const uint4*>(pairs + r + q)
+                              : *reinterpret_cast<const uint4*>(keys + r + q);
+        if (FIRST) {
+          kr[q] = x.x, j[q] = (int32_t)x.y, kr[q + 1] = x.z, j[q + 1] = (int32_t)x.w;
+        } else {
+          kr[q] = x.x, kr[q + 1] = x.y, kr[q + 2] = x.z, kr[q + 3] = x.w;
+        }
+      }
+      Pack<T, V> x[kRunIlp];
+#pragma unroll
+      for (int q = 0; q < kRunIlp; ++q) {
+        if (!FIRST) j[q] = kr[q] == kNoRow ? -1 : 0;
+        if (r + q >= b) j[q] = -1;
+        if (j[q] >= 0)
+          x[q] = *reinterpret_cast<const Pack<T, V>*>(g + (FIRST ? (int64_t)j[q] : r + q) * rs + c);
+      }
+#pragma unroll
+      for (int q = 0; q < kRunIlp; ++q) {
+        if (r + q >= b) break;
+        if (kr[q] != k) {
+          done(false);
+          k = kr[q];
+          head = false;
+          clear();
+        }
+        if (j[q] >= 0)
+#pragma unroll
+          for (int i = 0; i < V; ++i) sum[i] += to_f(x[q].x[i]);
       }
     }
-    Pack<T, V> x[kRunIlp];
-#pragma unroll
-    for (int q = 0; q < kRunIlp; ++q) {
-      if (!order) j[q] = kr[q] == kNoRow ? -1 : 0;
-      if (r + q >= b) j[q] = -1;
-      if (j[q] >= 0)
-        x[q] = *reinterpret_cast<const Pack<T, V>*>(g + (order ? (int64_t)j[q] : r + q) * rs + c);
-    }
-#pragma unroll
-    for (int q = 0; q < kRunIlp; ++q) {
-      if (r + q >= b) break;
-      if (kr[q] != k) {
-        done(false);
-        k = kr[q];
-        head = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = 0.f;
-      }
-      if (j[q] >= 0)
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += to_f(x[q].x[i]);
+    start = whole = false;  // of the last run: the first may have left a slot 0
+    done(b < n && key_at(b) == k);
+    if (tv == 0) {
+      s_start[team] = start;
+      s_whole[team] = whole;
     }
   }
-  done(b < n && keys[b] == k);
+  __syncthreads();
+  if (!on) return;
+  // runs that came into the block (team 0), and that start in this team
+  bool used0 = false, used1 = false;
+  const auto leave = [&](int slot, uint32_t key, bool zero) {
+    const int64_t p = 2 * blk + slot;
+    if (c == 0) pkey[p] = key;
+#pragma unroll
+    for (int i = 0; i < V; ++i) psum[p * ldp + c + i] = zero ? 0.f : sum[i];
+    (slot ? used1 : used0) = true;
+  };
+  const auto add_following = [&](int u) {  // -> true if the run leaves the block
+    for (; u < used; ++u) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += s_part[0][(u * width + tv) * V + i];
+      if (!s_whole[u]) return false;
+    }
+    return true;
+  };
+  const auto load = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = s_part[slot][t * V + i];
+  };
+  if (team == 0 && A > 0) {
+    const uint32_t first = key_at(A);
+    if (first != kNoRow && key_at(A - 1) == first) {
+      load(0);
+      const bool through = s_whole[0] && add_following(1);
+      leave(0, first, false);
+      if (through) leave(1, first, true);
+    }
+  }
+  bool tail = false;
+  if (s_start[team]) {
+    load(1);
+    tail = add_following(team + 1);
+    if (tail) leave(1, k, false);
+    else to_table(k);
+  }
+  // the partials that nothing set: entry 0 is team 0's, entry 1 whoever's run
+  // leaves the block
   if (c == 0) {
-    if (!used0) pkey[2 * chunk] = kNoRow;
-    if (!used1) pkey[2 * chunk + 1] = kNoRow;
+    if (team == 0 && !used0) pkey[2 * blk] = kNoRow;
+    if (team == used - 1) {
+      const uint32_t last = key_at(B - 1);
+      if (last == kNoRow || B == n || key_at(B) != last) pkey[2 * blk + 1] = kNoRow;
+    }
   }
 }
 
@@ -618,22 +831,10 @@ unsigned blocks_for(int64_t threads) { return (unsigned)((threads + kThreads - 1
 
 int key_bits(int64_t rows) { return rows > 1 ? 64 - __builtin_clzll((unsigned long long)(rows - 1)) : 0; }
 
-constexpr int kPartChunk = 64;  // entries per chunk of partials
-
-// Entries per chunk of the items: enough chunks to fill the device, and few
-// enough partials that they cost little.
-int chunk_of(int64_t n, int nv) {
-  const int64_t fill = n * nv / (148 * 1024);
-  int R = kRunIlp;
-  while (R < 128 && R < fill) R *= 2;
-  return R;
-}
-
 struct LookupWs {
-  uint32_t* keys;
-  int32_t* order;
-  void* sort;
-  size_t sort_bytes;
+  uint2* pairs[2];  // the sorted order ends in pairs[0]
+  uint32_t* counts;
+  uint32_t* total;
   uint32_t* pkey[2];
   float* psum[2];
   uint4* rows;  // the items' rows, for a gradient in planes
@@ -641,21 +842,36 @@ struct LookupWs {
   size_t bytes;
 };
 
+struct Passes {
+  int count, bits;
+  explicit Passes(int64_t rows) {
+    const int all = key_bits(rows);
+    count = all <= kMaxDigit ? 1 : (all + kMaxDigit - 1) / kMaxDigit;
+    bits = (all + count - 1) / count;
+  }
+};
+
 LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, int planes_es) {
   LookupWs w{};
   if (n <= kSmallItems) return w;
   Carver cv(ws, cap);
   w.ldp = (cols + 7) / 8 * 8;
-  w.keys = cv.take<uint32_t>(round_up(n, kRunIlp));
-  w.order = cv.take<int32_t>(round_up(n, kRunIlp));
-  w.sort_bytes = gs_sort_workspace_size(n, 4, 0, key_bits(rows));
-  w.sort = cv.take<char>(w.sort_bytes);
-  const int R = chunk_of(n, (cols + 7) / 8);  // the smallest that any type takes
-  int64_t m = 2 * ((n + R - 1) / R);
+  const Passes ps(rows);
+  w.pairs[0] = cv.take<uint2>(round_up(n, kRunIlp));
+  w.pairs[1] = cv.take<uint2>(ps.count > 1 ? n : 0);
+  w.counts = cv.take<uint32_t>(((size_t)1 << ps.bits) * ((n + kSortTile - 1) / kSortTile));
+  w.total = cv.take<uint32_t>((size_t)1 << ps.bits);
+  // partials: the most that any vector width leaves (the narrowest teams)
+  int64_t m = n;
   for (int k = 0; k < 2; ++k) {
+    int64_t most = 0;
+    for (int V = 1; V <= 8; V *= 2) {
+      const int64_t b = RunShape(m, cols, V, k ? kRunIlp : 0).blocks;
+      if (b > most) most = b;
+    }
+    m = 2 * most;
     w.pkey[k] = cv.take<uint32_t>(round_up(m, kRunIlp));
     w.psum[k] = cv.take<float>((size_t)m * w.ldp);
-    m = 2 * ((m + kPartChunk - 1) / kPartChunk);
   }
   if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
   w.bytes = cv.off;
@@ -682,34 +898,46 @@ gs_status check_ids(const int32_t* ids, int64_t n_ids, const int32_t* index, int
   return GS_OK;
 }
 
+// Sorts the items by id into w.pairs[0]; also clears `zeros` floats at dtable.
 gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, int64_t n,
-                      int64_t rows, const LookupWs& w, int32_t* dev_status, cudaStream_t s) {
-  GS_TRY(launch_dependent(k_lookup_keys, blocks_for(n), kThreads, 0, s, ids, n_ids, index, n, rows,
-                          w.keys, w.order, dev_status));
-  GS_LAUNCH_CHECK();
-  return gs_sort_keys32(nullptr, w.keys, w.order, n, 0, key_bits(rows), 0, w.sort, w.sort_bytes,
-                        dev_status, s);
+                      int64_t rows, const LookupWs& w, float* dtable, int64_t zeros,
+                      int32_t* dev_status, cudaStream_t s) {
+  const Passes ps(rows);
+  const Ids src{ids, index, n_ids, rows};
+  const unsigned tiles = (unsigned)((n + kSortTile - 1) / kSortTile);
+  for (int p = 0; p < ps.count; ++p) {
+    const uint2* from = w.pairs[(ps.count - p) & 1];
+    uint2* to = w.pairs[(ps.count - 1 - p) & 1];
+    const int shift = p * ps.bits;
+    GS_TRY(launch_dependent(p == 0 ? k_sort_count<true> : k_sort_count<false>, tiles, kThreads, 0, s,
+                            src, from, n, shift, ps.bits, w.counts, dtable, zeros, dev_status));
+    GS_LAUNCH_CHECK();
+    GS_TRY(launch_dependent(k_sort_scan, 1u << ps.bits, kThreads, 0, s, w.counts, tiles, w.total));
+    GS_LAUNCH_CHECK();
+    GS_TRY(launch_dependent(p == 0 ? k_sort_scatter<true> : k_sort_scatter<false>, tiles, kThreads,
+                            scatter_smem(ps.bits), s, src, from, n, shift, ps.bits, w.counts, w.total,
+                            to));
+    GS_LAUNCH_CHECK();
+  }
+  return GS_OK;
 }
 
 template <class T, int V>
 gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, float* dt, int64_t ld,
                    bool accumulate, const LookupWs& w, cudaStream_t s) {
-  const int nv = (cols + V - 1) / V;
-  int R = chunk_of(n, nv);
-  int64_t m = n, chunks = (m + R - 1) / R;
-  if (chunks * nv > (int64_t)INT32_MAX * kThreads) return GS_ERR_UNSUPPORTED;
-  GS_TRY(launch_dependent(k_run_sums<T, V>, blocks_for(chunks * nv), kThreads, 0, s, w.keys, w.order,
-                          m, R, g, rs, cols, Div((uint32_t)nv), scale, dt, ld, accumulate, w.pkey[0],
-                          w.psum[0], w.ldp));
+  RunShape sh(n, cols, V, 0);
+  if (sh.blocks * sh.col_tiles > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
+  GS_TRY(launch_dependent(k_run_sums<T, V, true>, (unsigned)(sh.blocks * sh.col_tiles), sh.threads, 0,
+                          s, w.pairs[0], nullptr, n, sh.len, sh.teams, sh.width, sh.col_tiles, g, rs,
+                          cols, scale, dt, ld, accumulate, w.pkey[0], w.psum[0], w.ldp));
   GS_LAUNCH_CHECK();
-  const int nv4 = (cols + 3) / 4;
-  for (int from = 0; chunks > 1; from ^= 1) {
-    m = 2 * chunks;
-    chunks = (m + kPartChunk - 1) / kPartChunk;
-    GS_TRY(launch_dependent(k_run_sums<float, 4>, blocks_for(chunks * nv4), kThreads, 0, s,
-                            w.pkey[from], nullptr, m, kPartChunk, w.psum[from], w.ldp, cols,
-                            Div((uint32_t)nv4), scale, dt, ld, accumulate, w.pkey[from ^ 1],
-                            w.psum[from ^ 1], w.ldp));
+  for (int from = 0; sh.blocks > 1; from ^= 1) {
+    const int64_t m = 2 * sh.blocks;
+    sh = RunShape(m, cols, 4, kRunIlp);
+    GS_TRY(launch_dependent(k_run_sums<float, 4, false>, (unsigned)(sh.blocks * sh.col_tiles),
+                            sh.threads, 0, s, nullptr, w.pkey[from], m, sh.len, sh.teams, sh.width,
+                            sh.col_tiles, w.psum[from], w.ldp, cols, scale, dt, ld, accumulate,
+                            w.pkey[from ^ 1], w.psum[from ^ 1], w.ldp));
     GS_LAUNCH_CHECK();
   }
   return GS_OK;
@@ -833,7 +1061,7 @@ extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int
   if (!ws || w.bytes > ws_bytes || ws_bytes < 256) return GS_ERR_CAPACITY;
   if (!aligned(ws, 256)) return GS_ERR_ARG;
   if (n <= kSmallItems) return GS_OK;  // such gradients need no order
-  return plan_lookup(ids, n_ids, index, n, rows, w, dev_status, to_stream(stream));
+  return plan_lookup(ids, n_ids, index, n, rows, w, nullptr, 0, dev_status, to_stream(stream));
 }
 
 namespace gs {
@@ -908,11 +1136,19 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
     if (!aligned(ws, 256)) return GS_ERR_ARG;
   }
   const bool accumulate = (flags & GS_LOOKUP_ACCUMULATE) != 0;
-  if (!accumulate && (n == 0 || n > kSmallItems))
-    GS_TRY(cudaMemset2DAsync(dtable->data, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
+  const bool plan = !(flags & GS_LOOKUP_PLANNED) && n > kSmallItems;
+  float* dt = static_cast<float*>(dtable->data);
+  // rows that no item uses: cleared by the sort's first kernel where the table
+  // is contiguous and no block of it gets more than 32 KB to clear
+  const int64_t elements = rows * dtable->cols, tiles = (n + kSortTile - 1) / kSortTile;
+  const bool fused = plan && !accumulate && dtable->row_stride == dtable->cols &&
+                     elements <= tiles * 8192;
+  if (!accumulate && !fused && (n == 0 || n > kSmallItems))
+    GS_TRY(cudaMemset2DAsync(dt, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
   if (n == 0) return GS_OK;
-  if (!(flags & GS_LOOKUP_PLANNED) && n > kSmallItems) {
-    const gs_status ps = plan_lookup(ids, n_ids, index, n, rows, w, dev_status, s);
+  if (plan) {
+    const gs_status ps = plan_lookup(ids, n_ids, index, n, rows, w, dt, fused ? elements : 0,
+                                     dev_status, s);
     if (ps != GS_OK) return ps;
   }
   const float sc = (float)scale;
