@@ -303,16 +303,11 @@ struct Ids {
   int64_t n_ids, rows;
 };
 
-__device__ __forceinline__ uint2 pair_of(const Ids& s, int64_t j, int32_t* dev_status) {
-  const int32_t id = id_of(s.ids, s.n_ids, s.index, j, s.rows, dev_status);
-  return id >= 0 ? make_uint2((uint32_t)id, (uint32_t)j)
-                 : make_uint2((uint32_t)(s.rows - 1), 0xffffffffu);
-}
-
-// counts[digit][tile]; the first pass also clears `zeros` floats of dtable
+// counts[digit][tile]; the first pass also writes the pairs and clears `zeros`
+// floats of dtable
 template <bool FIRST>
 __global__ void __launch_bounds__(kThreads)
-k_sort_count(const __grid_constant__ Ids src, const uint2* __restrict__ pairs, int64_t n, int shift,
+k_sort_count(const __grid_constant__ Ids src, uint2* __restrict__ pairs, int64_t n, int shift,
              int bits, uint32_t* __restrict__ counts, float* __restrict__ dtable, int64_t zeros,
              int32_t* dev_status) {
   __shared__ uint32_t s_hist[1 << kMaxDigit];
@@ -322,17 +317,45 @@ k_sort_count(const __grid_constant__ Ids src, const uint2* __restrict__ pairs, i
   __syncthreads();
   const int64_t j0 = (int64_t)blockIdx.x * kSortTile + t;
   uint32_t key[kSortItems];
+  if (FIRST) {
+    // all positions, then all ids in flight
+    int64_t at[kSortItems];
+    int32_t id[kSortItems];
+    bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kSortItems; ++i) {
-    const int64_t j = j0 + i * kThreads;
-    if (j < n) key[i] = FIRST ? pair_of(src, j, dev_status).x : pairs[j].x;
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t j = j0 + i * kThreads;
+      at[i] = j < n ? (src.index ? (int64_t)src.index[j] : j) : -2;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const bool in = at[i] >= 0 && (!src.index || at[i] < src.n_ids);
+      bad |= at[i] != -2 && !in;
+      id[i] = in ? src.ids[at[i]] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t j = j0 + i * kThreads;
+      if (id[i] >= src.rows) {
+        bad = true;
+        id[i] = -1;
+      }
+      key[i] = id[i] >= 0 ? (uint32_t)id[i] : (uint32_t)(src.rows - 1);
+      if (j < n) pairs[j] = make_uint2(key[i], id[i] >= 0 ? (uint32_t)j : 0xffffffffu);
+    }
+    if (bad) dev_flag(dev_status, GS_DEV_BOUNDS);
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < zeros; i += (int64_t)gridDim.x * kThreads)
+      dtable[i] = 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const int64_t j = j0 + i * kThreads;
+      if (j < n) key[i] = pairs[j].x;
+    }
   }
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i)
     if (j0 + i * kThreads < n) atomicAdd(&s_hist[(key[i] >> shift) & (bins - 1)], 1u);
-  if (FIRST)
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < zeros; i += (int64_t)gridDim.x * kThreads)
-      dtable[i] = 0.f;
   __syncthreads();
   for (int d = t; d < bins; d += kThreads) counts[(int64_t)d * gridDim.x + blockIdx.x] = s_hist[d];
 }
@@ -368,13 +391,13 @@ size_t scatter_smem(int bits) {
   return sizeof(uint2) * kSortTile + ((size_t)1 << bits) * (2 * sizeof(uint32_t) + 2 * (kThreads / 32));
 }
 
-template <bool FIRST>
-__global__ void __launch_bounds__(kThreads)
-k_sort_scatter(const __grid_constant__ Ids src, const uint2* __restrict__ pairs, int64_t n, int shift,
-               int bits, const uint32_t* __restrict__ counts, const uint32_t* __restrict__ total,
+__global__ void __launch_bounds__(kThreads, 5)
+k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
+               const uint32_t* __restrict__ counts, const uint32_t* __restrict__ total,
                uint2* __restrict__ out) {
+  constexpr int kWarps = kThreads / 32, kPer = (1 << kMaxDigit) / kThreads;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ uint32_t s_scan[kThreads / 32 + 1];
+  __shared__ unsigned long long s_scan[kWarps + 1];
   const int bins = 1 << bits;
   uint2* s_pair = reinterpret_cast<uint2*>(s_raw);
   uint32_t* s_loc = reinterpret_cast<uint32_t*>(s_pair + kSortTile);  // digit's start in the tile
@@ -382,52 +405,76 @@ k_sort_scatter(const __grid_constant__ Ids src, const uint2* __restrict__ pairs,
   uint16_t* s_hist = reinterpret_cast<uint16_t*>(s_base + bins);      // [warp][digit]
   wait_for_prior_grids();
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-  for (int i = t; i < bins * (kThreads / 32) / 2; i += kThreads) reinterpret_cast<uint32_t*>(s_hist)[i] = 0;
   const int64_t j0 = (int64_t)blockIdx.x * kSortTile;
   const int items = (int)min((int64_t)kSortTile, n - j0);
   uint2 p[kSortItems];
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {  // a warp's items are neighbours
     const int e = w * 32 * kSortItems + i * 32 + lane;
-    if (e < items) p[i] = FIRST ? pair_of(src, j0 + e, nullptr) : pairs[j0 + e];
+    if (e < items) p[i] = pairs[j0 + e];
     else p[i] = make_uint2(0xffffffffu, 0);  // behind the last item: behind all of the last digit
   }
+  // thread t has `per` neighbouring digits
+  const int per = (bins + kThreads - 1) / kThreads;
+  uint32_t tot[kPer], cnt[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int d = t * per + i;
+    const bool in = i < per && d < bins;
+    tot[i] = in ? total[d] : 0;
+    cnt[i] = in ? counts[(int64_t)d * gridDim.x + blockIdx.x] : 0;
+  }
+  for (int i = t; i < bins * kWarps / 2; i += kThreads) reinterpret_cast<uint32_t*>(s_hist)[i] = 0;
   __syncthreads();
   // rank of an item among its warp's items with the same digit
-  int rank[kSortItems];
+  uint16_t rank[kSortItems];
   uint16_t* hist = s_hist + w * bins;
+  unsigned same_of[kSortItems];
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) same_of[i] = 0xffffffffu;
+  for (int k = shift; k < shift + bits; ++k)
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const bool one = (p[i].x >> k) & 1;
+      const unsigned bal = __ballot_sync(0xffffffffu, one);
+      same_of[i] &= one ? bal : ~bal;
+    }
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {
     const uint32_t d = (p[i].x >> shift) & (bins - 1);
-    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const unsigned same = same_of[i];
     const int before = __popc(same & ((1u << lane) - 1)), had = hist[d];
-    rank[i] = had + before;
+    rank[i] = (uint16_t)(had + before);
     __syncwarp();
     if (before == 0) hist[d] = (uint16_t)(had + __popc(same));
     __syncwarp();
   }
   __syncthreads();
-  // digits' starts: thread t has `per` neighbouring digits
-  const int per = (bins + kThreads - 1) / kThreads;
   uint32_t local = 0, global = 0;
-  for (int d = t * per; d < min(bins, (t + 1) * per); ++d) {
-    uint32_t run = 0;
-    for (int k = 0; k < kThreads / 32; ++k) {
-      const uint32_t c = s_hist[k * bins + d];
-      s_hist[k * bins + d] = (uint16_t)run;
-      run += c;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int d = t * per + i;
+    if (i < per && d < bins) {
+      uint32_t run = 0;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const uint32_t c = s_hist[k * bins + d];
+        s_hist[k * bins + d] = (uint16_t)run;
+        run += c;
+      }
+      s_loc[d] = local;
+      s_base[d] = global + cnt[i];
+      local += run;
+      global += tot[i];
     }
-    s_loc[d] = local;
-    s_base[d] = global;
-    local += run;
-    global += total[d];
   }
-  uint32_t all;
-  const uint32_t local0 = block_exclusive_scan<uint32_t, kThreads / 32>(local, s_scan, &all);
-  const uint32_t global0 = block_exclusive_scan<uint32_t, kThreads / 32>(global, s_scan, &all);
+  // both scans at once: a tile has at most 2^11 items, the list less than 2^31
+  unsigned long long all;
+  const unsigned long long both = block_exclusive_scan<unsigned long long, kWarps>(
+      (unsigned long long)local << 32 | global, s_scan, &all);
   for (int d = t * per; d < min(bins, (t + 1) * per); ++d) {
-    s_loc[d] += local0;
-    s_base[d] += global0 + counts[(int64_t)d * gridDim.x + blockIdx.x] - s_loc[d];
+    s_loc[d] += (uint32_t)(both >> 32);
+    s_base[d] += (uint32_t)both - s_loc[d];
   }
   __syncthreads();
 #pragma unroll
@@ -436,56 +483,70 @@ k_sort_scatter(const __grid_constant__ Ids src, const uint2* __restrict__ pairs,
     s_pair[s_loc[d] + hist[d] + rank[i]] = p[i];
   }
   __syncthreads();
-  for (int i = t; i < items; i += kThreads) {
-    const uint2 x = s_pair[i];
-    out[s_base[(x.x >> shift) & (bins - 1)] + i] = x;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = t + k * kThreads;
+    if (i < items) {
+      const uint2 x = s_pair[i];
+      out[s_base[(x.x >> shift) & (bins - 1)] + i] = x;
+    }
   }
 }
 
 // Planes to rows (pitch `vecs` 16-byte vectors, columns past the last one
-// unset): the sums below read whole rows in the order of their ids, and a row
-// in planes costs a 32-byte sector for every element.  A warp turns 32 items
-// in its own part of shared memory; the rows leave as one contiguous piece.
+// zero): the sums below read whole rows in the order of their ids, and a row
+// in planes costs a 32-byte sector for every element.  A block copies
+// kTurnItems items of up to 192 bytes' columns into shared memory, a plane's
+// piece at a time, all in flight, and writes the rows as one contiguous piece.
+constexpr int kTurnItems = 256;
+
 template <class T>
-__global__ void __launch_bounds__(32 * kStageWarps)
+struct Turn {
+  static constexpr int V = 16 / sizeof(T), kVecs = 12, kCols = kVecs * V;
+  static constexpr int kPitch = kTurnItems + 4 / sizeof(T);  // odd in words
+  static constexpr size_t kSmem = sizeof(T) * kCols * kPitch;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
 k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4* __restrict__ out,
                  int vecs) {
-  constexpr int V = 16 / sizeof(T);
-  __shared__ __align__(16) uint32_t s_rows[kStageWarps][32 * kStagePitch];
+  constexpr int V = Turn<T>::V, kVecs = Turn<T>::kVecs, P = Turn<T>::kPitch, W = kThreads / 32;
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  T* s = reinterpret_cast<T*>(s_raw);
   wait_for_prior_grids();
-  const int lane = threadIdx.x & 31;
-  uint32_t* s = s_rows[threadIdx.x >> 5];
-  const int64_t j0 = ((int64_t)blockIdx.x * kStageWarps + (threadIdx.x >> 5)) * 32, j = j0 + lane;
-  if (j0 >= n) return;
-  const int items = (int)min((int64_t)32, n - j0);
-  for (int v0 = 0; v0 < vecs; v0 += kStageVecs) {
-    const int nv = min(kStageVecs, vecs - v0);
-    if (j < n) {
-      const T* p = g + (int64_t)v0 * V * cs + j;
-#pragma unroll 4
-      for (int q = 0; q < nv; ++q) {
-        union {
-          uint4 raw;
-          uint32_t w[4];
-        } x;
-        x.raw = make_uint4(0, 0, 0, 0);
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
+  const int items = (int)min((int64_t)kTurnItems, n - j0);
+  for (int v0 = 0; v0 < vecs; v0 += kVecs) {
+    const int nv = min(kVecs, vecs - v0), c0 = v0 * V;
+    for (int c = w; c < nv * V; c += W) {
+      const T* p = g + (int64_t)(c0 + c) * cs + j0;
+      T* d = s + c * P;
+      if (c0 + c >= cols) {
+        for (int j = lane; j < items; j += 32) d[j] = from_f<T>(0.f);
+      } else if (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if ((v0 + q) * V + i < cols) {
-            if (sizeof(T) == 4) x.w[i] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-            else x.w[i / 2] |= (uint32_t)__ldcs(reinterpret_cast<const uint16_t*>(p)) << (16 * (i & 1));
-          }
-          p += cs;
-        }
-        *reinterpret_cast<uint4*>(s + lane * kStagePitch + 4 * q) = x.raw;
+        for (int k = 0; k < kTurnItems / 32; ++k)
+          if (lane + 32 * k < items)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(d + lane + 32 * k)),
+                         "l"(p + lane + 32 * k)
+                         : "memory");
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTurnItems / 32; ++k)
+          if (lane + 32 * k < items) d[lane + 32 * k] = p[lane + 32 * k];
       }
     }
-    __syncwarp();
-    int r = lane / nv, v = lane - r * nv;
-    const int dr = 32 / nv, dv = 32 - dr * nv;
-    for (int k = 0; k < nv; ++k) {
-      if (r < items)
-        out[(j0 + r) * vecs + v0 + v] = *reinterpret_cast<const uint4*>(s + r * kStagePitch + 4 * v);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    int r = t / nv, v = t - r * nv;
+    const int dr = kThreads / nv, dv = kThreads - dr * nv;
+    for (int e = t; e < items * nv; e += kThreads) {
+      Pack<T, V> x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x.x[i] = s[(v * V + i) * P + r];
+      *reinterpret_cast<Pack<T, V>*>(out + (j0 + r) * vecs + v0 + v) = x;
       r += dr;
       v += dv;
       if (v >= nv) {
@@ -493,7 +554,7 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
         ++r;
       }
     }
-    __syncwarp();
+    __syncthreads();
   }
 }
 
@@ -858,7 +919,7 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   w.ldp = (cols + 7) / 8 * 8;
   const Passes ps(rows);
   w.pairs[0] = cv.take<uint2>(round_up(n, kRunIlp));
-  w.pairs[1] = cv.take<uint2>(ps.count > 1 ? n : 0);
+  w.pairs[1] = cv.take<uint2>(n);
   w.counts = cv.take<uint32_t>(((size_t)1 << ps.bits) * ((n + kSortTile - 1) / kSortTile));
   w.total = cv.take<uint32_t>((size_t)1 << ps.bits);
   // partials: the most that any vector width leaves (the narrowest teams)
@@ -906,7 +967,7 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
   const Ids src{ids, index, n_ids, rows};
   const unsigned tiles = (unsigned)((n + kSortTile - 1) / kSortTile);
   for (int p = 0; p < ps.count; ++p) {
-    const uint2* from = w.pairs[(ps.count - p) & 1];
+    uint2* from = w.pairs[(ps.count - p) & 1];
     uint2* to = w.pairs[(ps.count - 1 - p) & 1];
     const int shift = p * ps.bits;
     GS_TRY(launch_dependent(p == 0 ? k_sort_count<true> : k_sort_count<false>, tiles, kThreads, 0, s,
@@ -914,9 +975,8 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
     GS_LAUNCH_CHECK();
     GS_TRY(launch_dependent(k_sort_scan, 1u << ps.bits, kThreads, 0, s, w.counts, tiles, w.total));
     GS_LAUNCH_CHECK();
-    GS_TRY(launch_dependent(p == 0 ? k_sort_scatter<true> : k_sort_scatter<false>, tiles, kThreads,
-                            scatter_smem(ps.bits), s, src, from, n, shift, ps.bits, w.counts, w.total,
-                            to));
+    GS_TRY(launch_dependent(k_sort_scatter, tiles, kThreads, scatter_smem(ps.bits), s, from, n, shift,
+                            ps.bits, w.counts, w.total, to));
     GS_LAUNCH_CHECK();
   }
   return GS_OK;
@@ -1103,9 +1163,10 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
   const int64_t ld = dtable->row_stride;
   if (planes) {
     const int vecs = (cols + V - 1) / V;
-    GS_TRY(launch_dependent(k_planes_to_rows<T>,
-                            (unsigned)((n + 32 * kStageWarps - 1) / (32 * kStageWarps)),
-                            32 * kStageWarps, 0, s, data, g->col_stride, cols, n, w.rows, vecs));
+    static std::atomic<unsigned long long> once{0};
+    GS_TRY(smem_attrs_once((const void*)k_planes_to_rows<T>, (int)Turn<T>::kSmem, &once));
+    GS_TRY(launch_dependent(k_planes_to_rows<T>, (unsigned)((n + kTurnItems - 1) / kTurnItems),
+                            kThreads, Turn<T>::kSmem, s, data, g->col_stride, cols, n, w.rows, vecs));
     GS_LAUNCH_CHECK();
     return run_sums<T, V>(reinterpret_cast<const T*>(w.rows), (int64_t)vecs * V, n, cols, scale, dt,
                           ld, accumulate, w, s);
