@@ -223,17 +223,18 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
   }
 }
 
-// out in planes, rows of more than 32 bytes on 16-byte boundaries: a warp
-// fetches the rows of 32 items together (lanes along the row, so that a line
-// is one request; a lane that reads its own row makes one request for every
-// 32 bytes, which bounded the kernel above: 309 us against this one's at
-// 6M x 48) by asynchronous copies into its own part of shared memory, and
-// each lane then reads its item's row from there, 16 bytes at a time.  The
-// row pitch of 4 words more than a multiple of 16 keeps those reads free of
-// bank conflicts.  Many short blocks hide the latencies; persistent blocks
-// that fetch the next ids ahead took 293 us, these take 286.
-constexpr int kStageWarps = 4, kStageVecs = 12;            // 192 bytes of a row at a time
-constexpr int kStagePitch = 4 * kStageVecs + 4;            // words
+// out in planes, rows of more than 32 bytes on 16-byte boundaries: a block
+// fetches the rows of kTurnItems items (192 bytes of them at a time) into
+// shared memory by asynchronous copies with lanes along the rows, so that a
+// line is one request (a lane that reads its own row makes a request for
+// every 32 bytes: 309 us at 6M x 48), and a warp writes four (eight) planes'
+// pieces of 128 items from there, 16 bytes of a row at a time.  The row pitch
+// of 4 words more than a multiple of 16 keeps those reads free of bank
+// conflicts.  Pieces of a plane must be long: single warps that wrote 32
+// items of all planes in turn took 286 us.
+constexpr int kTurnItems = 256;
+constexpr int kStageVecs = 12, kStagePitch = 4 * kStageVecs + 4;  // words
+constexpr size_t kStageSmem = sizeof(uint32_t) * kTurnItems * kStagePitch;
 
 __device__ __forceinline__ void copy_16_async(void* smem, const void* p, bool has) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(p),
@@ -242,25 +243,28 @@ __device__ __forceinline__ void copy_16_async(void* smem, const void* p, bool ha
 }
 
 template <class TT, class TO>
-__global__ void __launch_bounds__(32 * kStageWarps)
+__global__ void __launch_bounds__(kThreads)
 k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, int cols,
                        const int32_t* __restrict__ ids, int64_t n_ids,
                        const int32_t* __restrict__ index, float scale, TO* __restrict__ out,
                        int64_t n, int64_t cs, int32_t* dev_status) {
-  constexpr int V = 16 / sizeof(TT);
-  __shared__ __align__(16) uint32_t s_rows[kStageWarps][32 * kStagePitch];
-  const int lane = threadIdx.x & 31;
-  uint32_t* s = s_rows[threadIdx.x >> 5];
-  const int64_t j = ((int64_t)blockIdx.x * kStageWarps + (threadIdx.x >> 5)) * 32 + lane;
-  const int32_t id = j < n ? id_of(ids, n_ids, index, j, rows, dev_status) : -1;
+  constexpr int V = 16 / sizeof(TT), W = kThreads / 32, PIECE = 128;
+  static_assert(kThreads == kTurnItems, "a thread for each item's id");
+  extern __shared__ __align__(16) uint32_t s_rows[];
+  __shared__ int32_t s_id[kTurnItems];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
+  const int items = (int)min((int64_t)kTurnItems, n - j0);
+  s_id[t] = t < items ? id_of(ids, n_ids, index, j0 + t, rows, dev_status) : -1;
+  __syncthreads();
   for (int c0 = 0; c0 < cols; c0 += kStageVecs * V) {
     const int nv = min(kStageVecs, (cols - c0) / V);
-    int r = lane / nv, v = lane - r * nv;
-    const int dr = 32 / nv, dv = 32 - dr * nv;
-    for (int k = 0; k < nv; ++k) {
-      const int32_t row = __shfl_sync(0xffffffffu, id, r);
-      copy_16_async(s + r * kStagePitch + 4 * v,
-                    table + (int64_t)(row < 0 ? 0 : row) * ld + c0 + v * V, row >= 0);
+    int r = t / nv, v = t - r * nv;
+    const int dr = kThreads / nv, dv = kThreads - dr * nv;
+    for (int e = t; e < items * nv; e += kThreads) {
+      const int32_t id = s_id[r];
+      copy_16_async(s_rows + r * kStagePitch + 4 * v,
+                    table + (int64_t)(id < 0 ? 0 : id) * ld + c0 + v * V, id >= 0);
       r += dr;
       v += dv;
       if (v >= nv) {
@@ -269,21 +273,23 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();
-    if (j < n) {
-      TO* o = out + (int64_t)c0 * cs + j;
-      for (int q = 0; q < nv; ++q) {
-        uint32_t w[4];
-        *reinterpret_cast<uint4*>(w) =
-            *reinterpret_cast<const uint4*>(s + lane * kStagePitch + 4 * q);
+    __syncthreads();
+    for (int u = w; u < nv * (kTurnItems / PIECE); u += W) {
+      const int q = u / (kTurnItems / PIECE);
+      TO* o = out + (int64_t)(c0 + q * V) * cs + j0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          *o = from_f<TO>(id >= 0 ? scale * element<TT>(w, i) : 0.f);
-          o += cs;
-        }
+      for (int k = 0; k < PIECE / 32; ++k) {
+        const int j = u % (kTurnItems / PIECE) * PIECE + k * 32 + lane;
+        if (j >= items) break;
+        uint32_t x[4];
+        *reinterpret_cast<uint4*>(x) =
+            *reinterpret_cast<const uint4*>(s_rows + j * kStagePitch + 4 * q);
+        const bool has = s_id[j] >= 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i * cs + j] = from_f<TO>(has ? scale * element<TT>(x, i) : 0.f);
       }
     }
-    __syncwarp();
+    __syncthreads();
   }
 }
 
@@ -498,8 +504,6 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
 // in planes costs a 32-byte sector for every element.  A block copies
 // kTurnItems items of up to 192 bytes' columns into shared memory, a plane's
 // piece at a time, all in flight, and writes the rows as one contiguous piece.
-constexpr int kTurnItems = 256;
-
 template <class T>
 struct Turn {
   static constexpr int V = 16 / sizeof(T), kVecs = 12, kCols = kVecs * V;
@@ -1034,10 +1038,11 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
     const int al = vector_of(t->data, t->row_stride, cols, sizeof(TT), 2 * V);
     const unsigned blocks = blocks_for(o->rows);
     if (al >= V && words > 8) {
-      const unsigned groups = (unsigned)((o->rows + 32 * kStageWarps - 1) / (32 * kStageWarps));
-      k_lookup_planes_staged<TT, TO><<<groups, 32 * kStageWarps, 0, s>>>(
-              static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index,
-              scale, static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status);
+      static std::atomic<unsigned long long> once{0};
+      GS_TRY(smem_attrs_once((const void*)k_lookup_planes_staged<TT, TO>, (int)kStageSmem, &once));
+      k_lookup_planes_staged<TT, TO><<<blocks, kThreads, kStageSmem, s>>>(
+          static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index, scale,
+          static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status);
       GS_LAUNCH_CHECK();
       return GS_OK;
     }
