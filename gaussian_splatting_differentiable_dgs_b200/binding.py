@@ -518,44 +518,57 @@ GS_LOOKUP_ACCUMULATE = 1
 GS_LOOKUP_PLANNED = 2
 
 
-def _dtypes():
+_codes = {}       # torch dtype -> GS_* element type, filled on first use
+_int32 = None
+_get_device = _raw_stream = None
+
+
+def _torch_names():
+    global _int32, _get_device, _raw_stream
     import torch
-    return {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16}
+    _codes.update({torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16})
+    _int32 = torch.int32
+    _get_device = torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class _OnDevice:
-    """Checks that tensors live on one CUDA device, and makes that device the
-    current one for the call (kernels and the default stream belong to it)."""
-
-    def __init__(self, name, *tensors):
+def _call(name, dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current: kernels, their attributes and the
+    default stream belong to a device."""
+    if dev == _get_device():
+        st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    else:
         import torch
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda or (dev is not None and t.get_device() != dev):
-                raise ValueError(f"{name}: tensors must be on one CUDA device")
-            dev = t.get_device()
-        self.guard = (torch.cuda.device(dev)
-                      if dev is not None and dev != torch.cuda.current_device() else None)
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    return st if st >= 0 else _ok(name, st)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _device(name, first, *rest):
+    """The CUDA device that all tensors (None allowed after the first) are on."""
+    if _int32 is None:
+        _torch_names()
+    dev = first.get_device()
+    ok = dev >= 0
+    for t in rest:
+        ok = ok and (t is None or t.get_device() == dev)
+    if not ok:
+        raise ValueError(f"{name}: tensors must be on one CUDA device")
+    return dev
 
 
 def matrix(t) -> gs_matrix:
     """Descriptor of a 2-D tensor: rows behind one another or planes (a
     transposed view of a planar buffer)."""
-    code = _dtypes().get(t.dtype)
-    if t.dim() != 2 or code is None:
+    if _int32 is None:
+        _torch_names()
+    code = _codes.get(t.dtype)
+    shape = t.shape
+    if code is None or len(shape) != 2:
         raise ValueError("a matrix is a 2-D float32, float16 or bfloat16 tensor, not "
                          f"{t.dim()}-D {t.dtype}")
-    rows, cols = t.shape
+    rows, cols = shape
     rs, cs = t.stride()
     # the stride of an axis of one element is arbitrary
     if cols == 1 and not (rs == 1 and cs >= rows):
@@ -568,10 +581,19 @@ def matrix(t) -> gs_matrix:
 
 
 def _ids(name, t):
-    import torch
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
+    if _int32 is None:
+        _torch_names()
+    if t.dtype is not _int32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
-    return t
+    return t.numel()
+
+
+def _items(ids, index, n):
+    """Checks ids and index; returns the number of ids."""
+    n_ids = _ids("ids", ids)
+    if index is not None and _ids("index", index) < n:
+        raise ValueError(f"index has {index.numel()} entries for {n} items")
+    return n_ids
 
 
 def _nbytes(ws):
@@ -581,13 +603,11 @@ def _nbytes(ws):
 def gs_lookup(table, ids, out, scale=1.0, index=None, dev_status=None, stream=None):
     """out[j] = scale * table[ids[j]] (or ids[index[j]]); out is written in the
     layout its strides say and returned."""
-    _ids("ids", ids), _ids("index", index)
-    if index is not None and index.numel() < out.shape[0]:
-        raise ValueError("index is shorter than out has rows")
-    with _OnDevice("gs_lookup", table, ids, out, index, dev_status):
-        _ok("gs_lookup", _L.gs_lookup(C.byref(matrix(table)), ptr(ids), ids.numel(), ptr(index),
-                                      float(scale), C.byref(matrix(out)), ptr(dev_status),
-                                      _stream(stream)))
+    t, o = matrix(table), matrix(out)
+    n_ids = _items(ids, index, o.rows)
+    dev = _device("gs_lookup", table, ids, out, index, dev_status)
+    _call("gs_lookup", dev, stream, _L.gs_lookup, t, ids.data_ptr(), n_ids, ptr(index), scale, o,
+          ptr(dev_status))
     return out
 
 
@@ -600,28 +620,22 @@ def gs_lookup_bwd_workspace_size(g, rows) -> int:
 
 def gs_lookup_plan(ids, n, rows, cols, ws, index=None, dev_status=None, stream=None):
     """Sorts n ids into ws for gs_lookup_bwd(..., planned=True)."""
-    _ids("ids", ids), _ids("index", index)
-    if index is not None and index.numel() < n:
-        raise ValueError("index is shorter than n")
-    with _OnDevice("gs_lookup_plan", ids, index, ws, dev_status):
-        return _ok("gs_lookup_plan", _L.gs_lookup_plan(
-            ptr(ids), ids.numel(), ptr(index), n, rows, cols, ptr(ws), _nbytes(ws),
-            ptr(dev_status), _stream(stream)))
+    n_ids = _items(ids, index, n)
+    dev = _device("gs_lookup_plan", ids, index, ws, dev_status)
+    return _call("gs_lookup_plan", dev, stream, _L.gs_lookup_plan, ids.data_ptr(), n_ids,
+                 ptr(index), n, rows, cols, ptr(ws), _nbytes(ws), ptr(dev_status))
 
 
 def gs_lookup_bwd(g, ids, dtable, ws, scale=1.0, index=None, accumulate=False, planned=False,
                   dev_status=None, stream=None):
     """dtable[k] (+)= scale * sum of g[j] over the items with id k; returns
     dtable."""
-    _ids("ids", ids), _ids("index", index)
-    if index is not None and index.numel() < g.shape[0]:
-        raise ValueError("index is shorter than g has rows")
+    m, d = matrix(g), matrix(dtable)
+    n_ids = _items(ids, index, m.rows)
     flags = (GS_LOOKUP_ACCUMULATE if accumulate else 0) | (GS_LOOKUP_PLANNED if planned else 0)
-    with _OnDevice("gs_lookup_bwd", g, ids, dtable, ws, index, dev_status):
-        _ok("gs_lookup_bwd", _L.gs_lookup_bwd(
-            C.byref(matrix(g)), ptr(ids), ids.numel(), ptr(index), float(scale),
-            C.byref(matrix(dtable)), flags, ptr(ws), _nbytes(ws), ptr(dev_status),
-            _stream(stream)))
+    dev = _device("gs_lookup_bwd", g, ids, dtable, ws, index, dev_status)
+    _call("gs_lookup_bwd", dev, stream, _L.gs_lookup_bwd, m, ids.data_ptr(), n_ids, ptr(index),
+          scale, d, flags, ptr(ws), _nbytes(ws), ptr(dev_status))
     return dtable
 
 
@@ -632,12 +646,15 @@ class TensorList:
     gs_grad_norm and gs_grad_clip."""
 
     def __init__(self, tensors):
-        codes = _dtypes()
+        if _int32 is None:
+            _torch_names()
         self.tensors = list(tensors)
         self.count = len(self.tensors)
         self.array = (gs_tensor * max(self.count, 1))()
+        self.shapes = [t.shape for t in self.tensors]
+        self.device = None  # the CUDA device of the tensors, -1 if they are not on one
         for k, t in enumerate(self.tensors):
-            code = codes.get(t.dtype)
+            code = _codes.get(t.dtype)
             if code is None:
                 raise ValueError(f"tensor {k}: {t.dtype} is not float32, float16 or bfloat16")
             if t.is_contiguous():
@@ -650,6 +667,8 @@ class TensorList:
                 raise ValueError(f"tensor {k} is neither contiguous nor rows of contiguous "
                                  f"elements (shape {tuple(t.shape)}, strides {t.stride()})")
             self.array[k] = gs_tensor(t.data_ptr(), rows, cols, rs, code, 0)
+            dev = t.get_device()
+            self.device = dev if self.device in (None, dev) else -1
 
 
 def tensor_list(tensors) -> TensorList:
@@ -662,33 +681,39 @@ def gs_grad_norm_workspace_size(tensors) -> int:
     return int(_L.gs_grad_norm_workspace_size(count))
 
 
+def _clip_device(name, clip, ws, dev_status, *lists):
+    import torch
+    if clip.dtype is not torch.float32 or clip.numel() < 2 or not clip.is_contiguous():
+        raise ValueError("clip must be a contiguous float32 tensor of 2 values")
+    dev = _device(name, clip, ws, dev_status)
+    for x in lists:
+        if x.device not in (None, dev):
+            raise ValueError(f"{name}: tensors must be on one CUDA device")
+    return dev
+
+
 def gs_grad_norm(tensors, max_norm, clip, ws, eps=1e-6, dev_status=None, stream=None):
     """clip[0] = global L2 norm, clip[1] = min(1, max_norm / (norm + eps))."""
-    import torch
     tl = tensor_list(tensors)
-    if clip.dtype != torch.float32 or clip.numel() < 2 or not clip.is_contiguous():
-        raise ValueError("clip must be a contiguous float32 tensor of 2 values")
-    with _OnDevice("gs_grad_norm", clip, ws, dev_status, *tl.tensors):
-        return _ok("gs_grad_norm", _L.gs_grad_norm(tl.array, tl.count, float(max_norm), float(eps),
-                                                   ptr(clip), ptr(ws), _nbytes(ws),
-                                                   ptr(dev_status), _stream(stream)))
+    dev = _clip_device("gs_grad_norm", clip, ws, dev_status, tl)
+    return _call("gs_grad_norm", dev, stream, _L.gs_grad_norm, tl.array, tl.count, max_norm, eps,
+                 clip.data_ptr(), ptr(ws), _nbytes(ws), ptr(dev_status))
 
 
 def gs_grad_clip(src, dst, clip, stream=None):
     """dst[i] = clip[1] * src[i] for lists of tensors (dst may be src)."""
     s, d = tensor_list(src), tensor_list(dst)
-    if s.count != d.count:
-        raise ValueError(f"{s.count} tensors to clip into {d.count}")
-    for x, y in zip(s.tensors, d.tensors):
-        if x.shape != y.shape:
-            raise ValueError(f"shape {tuple(x.shape)} to clip into {tuple(y.shape)}")
-    with _OnDevice("gs_grad_clip", clip, *s.tensors, *d.tensors):
-        return _ok("gs_grad_clip", _L.gs_grad_clip(s.array, d.array, s.count, ptr(clip),
-                                                   _stream(stream)))
+    if s.shapes != d.shapes:
+        raise ValueError(f"tensors of shapes {s.shapes} to clip into {d.shapes}")
+    dev = _clip_device("gs_grad_clip", clip, None, None, s, d)
+    return _call("gs_grad_clip", dev, stream, _L.gs_grad_clip, s.array, d.array, s.count,
+                 clip.data_ptr())
 
 
 def gs_adam_clipped(params, m, v, g, g_stride, slot, n, n_pad, P, args: gs_adam_args, clip,
                     stream=None):
-    return _ok("gs_adam_clipped", _L.gs_adam_clipped(
-        ptr(params), ptr(m), ptr(v), ptr(g), g_stride, ptr(slot), n, n_pad, P, C.byref(args),
-        ptr(clip), _stream(stream)))
+    """gs_adam on the gradient scaled by clip[1] (gs_grad_norm)."""
+    dev = _device("gs_adam_clipped", params, m, v, g, slot, clip)
+    return _call("gs_adam_clipped", dev, stream, _L.gs_adam_clipped, params.data_ptr(),
+                 m.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride, ptr(slot), n, n_pad, P, args,
+                 clip.data_ptr())

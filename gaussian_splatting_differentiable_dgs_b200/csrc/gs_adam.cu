@@ -285,6 +285,7 @@ k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__
                const float* __restrict__ g, int64_t g_stride, const int32_t* __restrict__ slot,
                bool g_vec, int64_t n, int64_t n_pad, int nP, unsigned col_blocks,
                const float* __restrict__ clip, AdamK a) {
+  wait_for_prior_grids();
   const int64_t i = ((int64_t)(blockIdx.x % col_blocks) * kThreads + threadIdx.x) * V;
   if (i >= n) return;
   const int plane0 = (int)(blockIdx.x / col_blocks) * kAdamPlanes;
@@ -786,17 +787,14 @@ extern "C" gs_status gs_adam_clipped(float* params, float* m, float* v, const fl
   // 16-byte vectors of p, m and v need planes and addresses that keep them
   // aligned; without them a thread owns one Gaussian
   const bool vec = (n_pad & 3) == 0 && aligned(params, 16) && aligned(m, 16) && aligned(v, 16);
-  const bool g_vec = !slot && (g_stride & 3) == 0 && aligned(g, 16);
+  const bool g_vec = vec && !slot && (g_stride & 3) == 0 && aligned(g, 16);
   const int64_t threads = vec ? (n + 3) / 4 : n;
   const int64_t col_blocks = (threads + kThreads - 1) / kThreads;
   const int64_t blocks = col_blocks * ((P + (int64_t)kAdamPlanes - 1) / kAdamPlanes);
   if (blocks > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
-  if (vec)
-    k_adam_clipped<4><<<(unsigned)blocks, kThreads, 0, to_stream(stream)>>>(
-        params, m, v, g, g_stride, slot, g_vec, n, n_pad, P, (unsigned)col_blocks, clip, a);
-  else
-    k_adam_clipped<1><<<(unsigned)blocks, kThreads, 0, to_stream(stream)>>>(
-        params, m, v, g, g_stride, slot, false, n, n_pad, P, (unsigned)col_blocks, clip, a);
+  GS_TRY(launch_dependent(vec ? k_adam_clipped<4> : k_adam_clipped<1>, (unsigned)blocks, kThreads, 0,
+                          to_stream(stream), params, m, v, g, g_stride, slot, g_vec, n, n_pad, P,
+                          (unsigned)col_blocks, clip, a));
   GS_LAUNCH_CHECK();
   return GS_OK;
 }

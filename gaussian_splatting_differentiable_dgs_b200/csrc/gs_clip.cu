@@ -19,6 +19,7 @@ constexpr int kUnitBytes = 16384;  // bytes of a row that a block takes at a tim
 constexpr int kFlatUnit = 4096;    // elements, where rows are too short for that
 constexpr int kShortRow = 1024;    // columns below which rows are short
 constexpr int kMaxTensors = 256;   // tensors per launch, passed by value
+constexpr int kFewTensors = 16;    // ... in a table that is quicker to pass
 constexpr int kNormBlocks = 148 * 8;
 constexpr int kClipBlocks = 148 * 8;
 
@@ -46,10 +47,11 @@ struct Entry {
   int32_t dtype;
 };
 
+template <int N>
 struct Table {
-  Entry t[kMaxTensors];
-  int32_t count;
   int64_t units;
+  int32_t count;
+  Entry t[N];
 };
 
 constexpr int kVecs = kUnitBytes / 16 / kThreads;  // vectors of a unit per thread
@@ -74,7 +76,7 @@ struct Stretch {
   // one(i): this thread's single elements before and behind the vectors
   template <class F>
   __device__ __forceinline__ void ends(F&& one) const {
-    const int t = threadIdx.x, tail = head + nv * (16 / (int)sizeof(T));
+    const int t = threadIdx.x % kThreads, tail = head + nv * (16 / (int)sizeof(T));
     if (t < head) one(t);
     if (t < len - tail) one(tail + t);
   }
@@ -84,7 +86,7 @@ struct Stretch {
 template <class T, class F>
 __device__ __forceinline__ void short_rows(const Entry& e, int64_t u, F&& one) {
   const int64_t a = (u - e.unit0) * kFlatUnit, b = min(a + kFlatUnit, e.size);
-  for (int64_t i = a + threadIdx.x; i < b; i += kThreads) {
+  for (int64_t i = a + threadIdx.x % kThreads; i < b; i += kThreads) {
     const int64_t r = i / e.cols, c = i - r * e.cols;
     one(static_cast<const T*>(e.src) + r * e.src_stride + c,
         static_cast<T*>(e.dst) + r * e.dst_stride + c);
@@ -92,9 +94,9 @@ __device__ __forceinline__ void short_rows(const Entry& e, int64_t u, F&& one) {
 }
 
 // f(tensor, unit) for this block's units, in turn from the first or the last
-template <bool BACK, class F>
-__device__ __forceinline__ void each_unit(const Table& tab, F&& f) {
-  for (int64_t k = blockIdx.x; k < tab.units; k += gridDim.x) {
+template <bool BACK, int N, class F>
+__device__ __forceinline__ void each_unit(const Table<N>& tab, int64_t first, int64_t step, F&& f) {
+  for (int64_t k = first; k < tab.units; k += step) {
     const int64_t u = BACK ? tab.units - 1 - k : k;
     int lo = 0, hi = tab.count - 1;  // the last tensor with unit0 <= u
     while (lo < hi) {
@@ -106,12 +108,12 @@ __device__ __forceinline__ void each_unit(const Table& tab, F&& f) {
   }
 }
 
-// Sums of squares in fp64: a square of a finite fp32 value neither overflows
-// nor vanishes there, and a sum over 2^40 elements keeps 1e-4 of its last
-// fp32 place.
-__global__ void __launch_bounds__(kThreads)
-k_sum_squares(const __grid_constant__ Table tab, double* __restrict__ part) {
-  __shared__ double s_warp[kThreads / 32];
+// Sum of squares of this thread's elements of the units first, first + step,
+// ..., a unit by kThreads threads.  fp64: a square of a finite fp32 value
+// neither overflows nor vanishes there, and a sum over 2^40 elements keeps
+// 1e-4 of its last fp32 place.
+template <int N>
+__device__ __forceinline__ double sum_squares(const Table<N>& tab, int64_t first, int64_t step) {
   double sum = 0.0;
   auto unit = [&](auto zero, const Entry& e, int64_t u) {
     using T = decltype(zero);
@@ -122,7 +124,7 @@ k_sum_squares(const __grid_constant__ Table tab, double* __restrict__ part) {
     Vec<T> buf[kVecs];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      const int i = threadIdx.x + k * kThreads;
+      const int i = threadIdx.x % kThreads + k * kThreads;
       buf[k].raw = i < x.nv ? __ldg(reinterpret_cast<const uint4*>(x.src + x.head) + i)
                             : make_uint4(0, 0, 0, 0);
     }
@@ -132,44 +134,99 @@ k_sum_squares(const __grid_constant__ Table tab, double* __restrict__ part) {
 #pragma unroll
       for (int i = 0; i < V; ++i) add(to_f(buf[k].x[i]));
   };
-  each_unit<false>(tab, [&](const Entry& e, int64_t u) {
+  each_unit<false>(tab, first, step, [&](const Entry& e, int64_t u) {
     if (e.dtype == GS_F32) unit(0.f, e, u);
     else if (e.dtype == GS_F16) unit(__half(), e, u);
     else unit(__nv_bfloat16(), e, u);
   });
-  sum = warp_sum(sum);
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) sum += s_warp[w];
-    part[blockIdx.x] = sum;
-  }
+  return sum;
 }
 
-// clip[0] = norm, clip[1] = coefficient (see gs.h for non-finite norms)
-__global__ void __launch_bounds__(kThreads)
-k_clip_coef(const double* __restrict__ part, int n, double max_norm, double eps,
-            float* __restrict__ clip, int32_t* dev_status) {
-  __shared__ double s_warp[kThreads / 32];
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) sum += part[i];
+// Sum over the block, valid in thread 0.
+template <int WARPS>
+__device__ __forceinline__ double block_sum(double sum, double* s_warp) {
   sum = warp_sum(sum);
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = sum;
   __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < WARPS; ++w) sum += s_warp[w];
+  return sum;
+}
+
+struct CoefArgs {
+  double max_norm, eps;
+  float* clip;
+  int32_t* dev_status;
+};
+
+// clip[0] = norm, clip[1] = coefficient (see gs.h for non-finite norms)
+__device__ __forceinline__ void write_clip(double sum, const CoefArgs& a) {
+  const double norm = sqrt(sum);
+  const double c = a.max_norm / (norm + a.eps);
+  a.clip[0] = (float)norm;
+  a.clip[1] = (float)(c < 1.0 ? c : isnan(norm) ? norm : 1.0);
+  if (!isfinite(norm)) dev_flag(a.dev_status, GS_DEV_NONFINITE);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+k_sum_squares(const __grid_constant__ Table<N> tab, double* __restrict__ part) {
+  __shared__ double s_warp[kThreads / 32];
+  wait_for_prior_grids();
+  const double sum = block_sum<kThreads / 32>(sum_squares(tab, blockIdx.x, gridDim.x), s_warp);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kThreads)
+k_clip_coef(const double* __restrict__ part, int n, const CoefArgs a) {
+  __shared__ double s_warp[kThreads / 32];
+  wait_for_prior_grids();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) sum += part[i];
+  sum = block_sum<kThreads / 32>(sum, s_warp);
+  if (threadIdx.x == 0) write_clip(sum, a);
+}
+
+// Up to kClusterUnits units in one launch: a cluster of 8 blocks, four units
+// at a time each; the blocks' sums meet in the first one's shared memory.
+// Two launches cost 2 us more, and a cluster alone draws too little bandwidth
+// for more than that.
+constexpr int kCluster = 8, kClusterThreads = 1024;
+constexpr int kClusterUnits = 2 * kCluster * kClusterThreads / kThreads;
+template <int N>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+k_norm_cluster(const __grid_constant__ Table<N> tab, const CoefArgs a) {
+  constexpr int G = kClusterThreads / kThreads;
+  __shared__ double s_warp[kClusterThreads / 32];
+  __shared__ double s_block[kCluster];
+  // every block has started before one writes to another's shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  wait_for_prior_grids();
+  const double sum = block_sum<kClusterThreads / 32>(
+      sum_squares(tab, blockIdx.x * G + threadIdx.x / kThreads, kCluster * G), s_warp);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) sum += s_warp[w];
-    const double norm = sqrt(sum);
-    const double c = max_norm / (norm + eps);
-    clip[0] = (float)norm;
-    clip[1] = (float)(c < 1.0 ? c : isnan(norm) ? norm : 1.0);
-    if (!isfinite(norm)) dev_flag(dev_status, GS_DEV_NONFINITE);
+    unsigned to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(&s_block[blockIdx.x])));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(sum) : "memory");
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    double all = 0.0;
+    for (int k = 0; k < kCluster; ++k) all += s_block[k];
+    write_clip(all, a);
   }
 }
 
 // The units are taken from the last to the first: what the norm read last is
 // still in L2.
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-k_clip(const __grid_constant__ Table tab, const float* __restrict__ clip) {
+k_clip(const __grid_constant__ Table<N> tab, const float* __restrict__ clip) {
+  wait_for_prior_grids();
   const float c = clip[1];
   auto unit = [&](auto zero, const Entry& e, int64_t u) {
     using T = decltype(zero);
@@ -200,7 +257,7 @@ k_clip(const __grid_constant__ Table tab, const float* __restrict__ clip) {
       }
     }
   };
-  each_unit<true>(tab, [&](const Entry& e, int64_t u) {
+  each_unit<true>(tab, blockIdx.x, gridDim.x, [&](const Entry& e, int64_t u) {
     if (c == 1.0f && e.src == e.dst) return;  // in place and nothing to clip
     if (e.dtype == GS_F32) unit(0.f, e, u);
     else if (e.dtype == GS_F16) unit(__half(), e, u);
@@ -250,12 +307,13 @@ bool pair_up(gs_tensor* a, gs_tensor* b) {
   return a->rows == b->rows && a->cols == b->cols;
 }
 
-// Fills tab with up to kMaxTensors non-empty tensors from *at on; false if one
+// Fills tab with up to N non-empty tensors from *at on; false if one
 // has rows of more units than 32 bits count.
-bool fill(Table& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count, int32_t* at) {
+template <int N>
+bool fill(Table<N>& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count, int32_t* at) {
   tab.count = 0;
   tab.units = 0;
-  for (; *at < count && tab.count < kMaxTensors; ++*at) {
+  for (; *at < count && tab.count < N; ++*at) {
     gs_tensor t = src[*at], d = dst ? dst[*at] : t;
     if (t.rows == 0 || t.cols == 0) continue;
     pair_up(&t, &d);
@@ -277,6 +335,43 @@ bool fill(Table& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count,
   return true;
 }
 
+template <int N>
+gs_status norm_impl(const gs_tensor* tensors, int32_t count, double* part, const CoefArgs& a,
+                    cudaStream_t s) {
+  Table<N> tab;
+  int parts = 0;
+  for (int32_t at = 0; at < count;) {
+    if (!fill(tab, tensors, nullptr, count, &at)) return GS_ERR_UNSUPPORTED;
+    if (tab.units <= kClusterUnits && at == count && parts == 0) {
+      GS_TRY(launch_dependent(k_norm_cluster<N>, kCluster, kClusterThreads, 0, s, tab, a));
+      GS_LAUNCH_CHECK();
+      return GS_OK;
+    }
+    if (tab.count == 0) break;
+    const unsigned blocks = (unsigned)(tab.units < kNormBlocks ? tab.units : kNormBlocks);
+    GS_TRY(launch_dependent(k_sum_squares<N>, blocks, kThreads, 0, s, tab, part + parts));
+    GS_LAUNCH_CHECK();
+    parts += (int)blocks;
+  }
+  GS_TRY(launch_dependent(k_clip_coef, 1, kThreads, 0, s, part, parts, a));
+  GS_LAUNCH_CHECK();
+  return GS_OK;
+}
+
+template <int N>
+gs_status clip_impl(const gs_tensor* src, const gs_tensor* dst, int32_t count, const float* clip,
+                    cudaStream_t s) {
+  Table<N> tab;
+  for (int32_t at = 0; at < count;) {
+    if (!fill(tab, src, dst, count, &at)) return GS_ERR_UNSUPPORTED;
+    if (tab.count == 0) break;
+    const unsigned blocks = (unsigned)(tab.units < kClipBlocks ? tab.units : kClipBlocks);
+    GS_TRY(launch_dependent(k_clip<N>, blocks, kThreads, 0, s, tab, clip));
+    GS_LAUNCH_CHECK();
+  }
+  return GS_OK;
+}
+
 }  // namespace
 }  // namespace gs
 
@@ -295,21 +390,10 @@ extern "C" gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, doubl
   if (!(max_norm >= 0) || !isfinite(max_norm) || !(eps >= 0) || !isfinite(eps)) return GS_ERR_ARG;
   if (!ws || ws_bytes < gs_grad_norm_workspace_size(count)) return GS_ERR_CAPACITY;
   if (!aligned(ws, 256)) return GS_ERR_ARG;
-  cudaStream_t s = to_stream(stream);
+  const CoefArgs a{max_norm, eps, clip, dev_status};
   double* part = static_cast<double*>(ws);
-  int parts = 0;
-  static thread_local Table tab;
-  for (int32_t at = 0; at < count;) {
-    if (!fill(tab, tensors, nullptr, count, &at)) return GS_ERR_UNSUPPORTED;
-    if (tab.count == 0) break;
-    const unsigned blocks = (unsigned)(tab.units < kNormBlocks ? tab.units : kNormBlocks);
-    k_sum_squares<<<blocks, kThreads, 0, s>>>(tab, part + parts);
-    GS_LAUNCH_CHECK();
-    parts += (int)blocks;
-  }
-  k_clip_coef<<<1, kThreads, 0, s>>>(part, parts, max_norm, eps, clip, dev_status);
-  GS_LAUNCH_CHECK();
-  return GS_OK;
+  return count <= kFewTensors ? norm_impl<kFewTensors>(tensors, count, part, a, to_stream(stream))
+                              : norm_impl<kMaxTensors>(tensors, count, part, a, to_stream(stream));
 }
 
 extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, int32_t count,
@@ -325,14 +409,6 @@ extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, in
     if (a == b && x.row_stride == y.row_stride) continue;
     if (extent(x) && a < b + extent(y) && b < a + extent(x)) return GS_ERR_ARG;
   }
-  cudaStream_t s = to_stream(stream);
-  static thread_local Table tab;
-  for (int32_t at = 0; at < count;) {
-    if (!fill(tab, src, dst, count, &at)) return GS_ERR_UNSUPPORTED;
-    if (tab.count == 0) break;
-    const unsigned blocks = (unsigned)(tab.units < kClipBlocks ? tab.units : kClipBlocks);
-    k_clip<<<blocks, kThreads, 0, s>>>(tab, clip);
-    GS_LAUNCH_CHECK();
-  }
-  return GS_OK;
+  return count <= kFewTensors ? clip_impl<kFewTensors>(src, dst, count, clip, to_stream(stream))
+                              : clip_impl<kMaxTensors>(src, dst, count, clip, to_stream(stream));
 }

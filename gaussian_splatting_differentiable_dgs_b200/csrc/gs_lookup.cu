@@ -82,6 +82,7 @@ k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
               const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index,
               float scale, TO* __restrict__ out, int64_t n, int64_t rs, Div nv, int items,
               int32_t* dev_status) {
+  wait_for_prior_grids();
   const int64_t j0 = (int64_t)blockIdx.x * items;  // items per block
   const uint32_t total = (uint32_t)min((int64_t)items, n - j0) * nv.d;
   for (uint32_t e0 = threadIdx.x; e0 < total; e0 += kThreads * kRowIlp) {
@@ -197,6 +198,7 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
                 float scale, TO* __restrict__ out, int64_t n, int64_t cs, int32_t* dev_status) {
   constexpr int C = NW * 4 / sizeof(TT);           // columns at a time
   constexpr int NL = ALIGNED ? NW : NW + 4;        // words loaded
+  wait_for_prior_grids();
   const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (j >= n) return;
   const int32_t id = id_of(ids, n_ids, index, j, rows, dev_status);
@@ -252,6 +254,7 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   static_assert(kThreads == kTurnItems, "a thread for each item's id");
   extern __shared__ __align__(16) uint32_t s_rows[];
   __shared__ int32_t s_id[kTurnItems];
+  wait_for_prior_grids();
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
   const int items = (int)min((int64_t)kTurnItems, n - j0);
@@ -1022,9 +1025,10 @@ gs_status launch_rows(const gs_matrix* t, const int32_t* ids, int64_t n_ids, con
   int items = kThreads * kRowIlp / nv;
   if (items < 1) items = 1;
   const int64_t blocks = (o->rows + items - 1) / items;
-  k_lookup_rows<TT, TO, V><<<(unsigned)blocks, kThreads, 0, s>>>(
-      static_cast<const TT*>(t->data), t->row_stride, t->rows, ids, n_ids, index, scale,
-      static_cast<TO*>(o->data), o->rows, o->row_stride, Div((uint32_t)nv), items, dev_status);
+  GS_TRY(launch_dependent(k_lookup_rows<TT, TO, V>, (unsigned)blocks, kThreads, 0, s,
+                          static_cast<const TT*>(t->data), t->row_stride, t->rows, ids, n_ids, index,
+                          scale, static_cast<TO*>(o->data), o->rows, o->row_stride,
+                          Div((uint32_t)nv), items, dev_status));
   GS_LAUNCH_CHECK();
   return GS_OK;
 }
@@ -1040,16 +1044,18 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
     if (al >= V && words > 8) {
       static std::atomic<unsigned long long> once{0};
       GS_TRY(smem_attrs_once((const void*)k_lookup_planes_staged<TT, TO>, (int)kStageSmem, &once));
-      k_lookup_planes_staged<TT, TO><<<blocks, kThreads, kStageSmem, s>>>(
-          static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index, scale,
-          static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status);
+      GS_TRY(launch_dependent(k_lookup_planes_staged<TT, TO>, blocks, kThreads, kStageSmem, s,
+                              static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids,
+                              n_ids, index, scale, static_cast<TO*>(o->data), o->rows,
+                              o->col_stride, dev_status));
       GS_LAUNCH_CHECK();
       return GS_OK;
     }
-#define GS_LOOKUP_PLANES(NW, AL)                                                              \
-  k_lookup_planes<TT, TO, NW, AL><<<blocks, kThreads, 0, s>>>(                                \
-      static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids, n_ids, index, scale, \
-      static_cast<TO*>(o->data), o->rows, o->col_stride, dev_status)
+#define GS_LOOKUP_PLANES(NW, AL)                                                                  \
+  GS_TRY(launch_dependent(k_lookup_planes<TT, TO, NW, AL>, blocks, kThreads, 0, s,                 \
+                          static_cast<const TT*>(t->data), t->row_stride, t->rows, cols, ids,      \
+                          n_ids, index, scale, static_cast<TO*>(o->data), o->rows, o->col_stride, \
+                          dev_status))
     if (words <= 16) {
       if (al == 2 * V) GS_LOOKUP_PLANES(16, 32);
       else if (al == V) GS_LOOKUP_PLANES(16, 16);
