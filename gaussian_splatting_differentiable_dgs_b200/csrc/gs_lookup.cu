@@ -567,53 +567,99 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
 
 // Sums of runs of equal keys over a list of n entries: the sorted items
 // (FIRST: pairs of a key and a row of g) or partials (keys, entry r being row
-// r).  A block takes a stretch of the list, a team of `width` threads (V
-// columns each) `len` entries of it, kRunIlp rows in flight.  A run inside a
-// team's entries goes to dtable.  What a team holds of a run that crosses its
-// borders goes to shared memory: slot 0 if the run came in from before, else
-// slot 1; the team in which a run starts then adds the following teams' slots
-// 0 in order.  Runs that cross the block's borders leave as partials: entry
-// 2 block for a run that came in, 2 block + 1 for one that starts here and
-// goes on; a block inside one run writes its sum at 2 block and zeros at
+// r).  A block takes E entries and copies their rows (`width` vectors of V
+// columns) into shared memory, all in flight at once without a register held;
+// then teams of `width` threads sum `len` entries each from there.  A run
+// inside a team's entries goes to dtable.  What a team holds of a run that
+// crosses its borders goes to a slot: slot 0 if the run came in from before,
+// else slot 1; the team in which a run starts then adds the following teams'
+// slots 0 in order.  Runs that cross the block's borders leave as partials:
+// entry 2 block for a run that came in, 2 block + 1 for one that starts here
+// and goes on; a block inside one run writes its sum at 2 block and zeros at
 // 2 block + 1, so that a run's partials are neighbours.  Unused partials have
 // the key kNoRow.  The same kernel sums the partials until one block is left.
-// Lists are readable up to a multiple of kRunIlp entries.
-constexpr int kRunIlp = 8, kMaxTeams = 64;
+constexpr int kMaxTeams = 128, kRunRowBytes = 40 * 1024, kRunEntries = 1024;
 
 struct RunShape {
-  int width, teams, threads, len, col_tiles;
+  int width, pitch, teams, entries, len, col_tiles, smem;  // pitch in bytes
   int64_t blocks;
-  RunShape(int64_t n, int cols, int V, int len0) : len(len0) {
-    const int nv = (cols + V - 1) / V;
-    width = nv < kThreads ? nv : kThreads;
+  RunShape(int64_t n, int cols, int V, int es, bool first) {
+    const int nv = (cols + V - 1) / V, most = V == 1 ? 64 : 16;
+    col_tiles = (nv + most - 1) / most;
+    width = (nv + col_tiles - 1) / col_tiles;
+    pitch = V == 1 ? (width * es + 3) / 4 * 4 : 16 * (width | 1);
     teams = kThreads / width < kMaxTeams ? kThreads / width : kMaxTeams;
-    threads = (teams * width + 31) / 32 * 32;
-    col_tiles = (nv + width - 1) / width;
-    // long stretches while they leave eight blocks for each SM
-    if (!len)
-      for (len = kRunIlp; len < 64 && n / (2 * len * teams) >= 148 * 8; len *= 2) {
-      }
-    blocks = (n + (int64_t)len * teams - 1) / ((int64_t)len * teams);
+    // what fits, for the items no more than leaves eight blocks for each SM
+    int64_t e = kRunRowBytes / pitch, fill = n / (148 * 8);
+    if (e > kRunEntries) e = kRunEntries;
+    if (first && e > fill) e = fill < 64 ? 64 : fill;
+    entries = (int)e;
+    len = (entries + teams - 1) / teams;
+    blocks = (n + entries - 1) / entries;
+    smem = (entries * pitch + 15) / 16 * 16 + 2 * kThreads * V * 4 + entries * 8;
   }
 };
 
 template <class T, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
-k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, int64_t n, int len,
-           int teams, int width, int col_tiles, const T* __restrict__ g, int64_t rs, int cols,
+k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, int64_t n,
+           const __grid_constant__ RunShape sh, const T* __restrict__ g, int64_t rs, int cols,
            float scale, float* __restrict__ dtable, int64_t ld, bool accumulate,
            uint32_t* __restrict__ pkey, float* __restrict__ psum, int ldp) {
-  __shared__ __align__(16) float s_part[2][kThreads * V];
+  extern __shared__ __align__(16) unsigned char s_row[];  // [entries][pitch]
   __shared__ bool s_start[kMaxTeams], s_whole[kMaxTeams];
+  const int pitch = sh.pitch, len = sh.len;
+  float* s_part = reinterpret_cast<float*>(s_row + (sh.entries * pitch + 15) / 16 * 16);
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_part + 2 * kThreads * V);
+  int32_t* s_item = reinterpret_cast<int32_t*>(s_key + sh.entries);
   wait_for_prior_grids();
-  const int t = threadIdx.x, team = t / width, tv = t - team * width;
-  const int64_t blk = blockIdx.x / col_tiles;
-  const int c = ((int)(blockIdx.x % col_tiles) * width + tv) * V;
-  const int64_t A = blk * teams * len, B = min(A + (int64_t)teams * len, n);
-  const int used = (int)((B - A + len - 1) / len);  // teams with entries
-  const int64_t a = A + (int64_t)team * len, b = min(a + len, B);
-  const bool on = team < used && c < cols;
+  const int t = threadIdx.x;
+  const int64_t blk = blockIdx.x / sh.col_tiles, A = blk * sh.entries;
+  const int m = (int)min((int64_t)sh.entries, n - A);
+  const int v0 = (int)(blockIdx.x % sh.col_tiles) * sh.width;
+  const int width = min(sh.width, (cols + V - 1) / V - v0);
+  for (int i = t; i < m; i += kThreads) {
+    if (FIRST) {
+      const uint2 p = pairs[A + i];
+      s_key[i] = p.x;
+      s_item[i] = (int32_t)p.y;
+    } else {
+      s_key[i] = keys[A + i];
+    }
+  }
   const auto key_at = [&](int64_t r) { return FIRST ? pairs[r].x : keys[r]; };
+  const uint32_t before = A > 0 ? key_at(A - 1) : kNoRow, after = A + m < n ? key_at(A + m) : kNoRow;
+  __syncthreads();
+  {
+    int r = t / width, v = t - r * width;
+    const int dr = kThreads / width, dv = kThreads - dr * width;
+    for (int e = t; e < m * width; e += kThreads) {
+      const int64_t j = FIRST ? (int64_t)s_item[r] : A + r;
+      const bool has = FIRST ? j >= 0 : s_key[r] != kNoRow;
+      const T* from = g + (has ? j : 0) * rs + (v0 + v) * V;
+      if (V > 1) {
+        copy_16_async(s_row + r * pitch + 16 * v, from, has);
+      } else if (sizeof(T) == 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         smem_addr(s_row + r * pitch + 4 * v)),
+                     "l"(from), "r"(has ? 4 : 0)
+                     : "memory");
+      } else {
+        reinterpret_cast<T*>(s_row + r * pitch)[v] = has ? *from : from_f<T>(0.f);
+      }
+      r += dr;
+      v += dv;
+      if (v >= width) {
+        v -= width;
+        ++r;
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  const int used = (m + len - 1) / len;  // teams with entries
+  const int team = t / width, tv = t - team * width, c = (v0 + tv) * V;
+  const bool on = team < used;  // m <= teams * len of the full width, and width is at most that
   uint32_t k = kNoRow;
   bool head = false, start = false, whole = false;
   float sum[V];
@@ -630,52 +676,31 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   const auto done = [&](bool tail) {
     if (k == kNoRow) return;
     if (!head && !tail) return to_table(k);
+    float* slot = s_part + (head ? 0 : kThreads * V) + t * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_part[head ? 0 : 1][t * V + i] = sum[i];
+    for (int i = 0; i < V; ++i) slot[i] = sum[i];
     start = !head;
     whole = head && tail;
   };
   if (on) {
-    k = key_at(a);
-    head = a > 0 && key_at(a - 1) == k && k != kNoRow;
+    const int a = team * len, b = min(a + len, m);
+    k = s_key[a];
+    head = k == (a > 0 ? s_key[a - 1] : before) && k != kNoRow;
     clear();
-    for (int64_t r = a; r < b; r += kRunIlp) {
-      uint32_t kr[kRunIlp];
-      int32_t j[kRunIlp];
-#pragma unroll
-      for (int q = 0; q < kRunIlp; q += FIRST ? 2 : 4) {
-        const uint4 x = FIRST ? *reinterpret_cast<const uint4*>(pairs + r + q)
-                              : *reinterpret_cast<const uint4*>(keys + r + q);
-        if (FIRST) {
-          kr[q] = x.x, j[q] = (int32_t)x.y, kr[q + 1] = x.z, j[q + 1] = (int32_t)x.w;
-        } else {
-          kr[q] = x.x, kr[q + 1] = x.y, kr[q + 2] = x.z, kr[q + 3] = x.w;
-        }
-      }
-      Pack<T, V> x[kRunIlp];
-#pragma unroll
-      for (int q = 0; q < kRunIlp; ++q) {
-        if (!FIRST) j[q] = kr[q] == kNoRow ? -1 : 0;
-        if (r + q >= b) j[q] = -1;
-        if (j[q] >= 0)
-          x[q] = *reinterpret_cast<const Pack<T, V>*>(g + (FIRST ? (int64_t)j[q] : r + q) * rs + c);
+    for (int r = a; r < b; ++r) {
+      const uint32_t kr = s_key[r];
+      const Pack<T, V> x = *reinterpret_cast<const Pack<T, V>*>(s_row + r * pitch + tv * V * sizeof(T));
+      if (kr != k) {
+        done(false);
+        k = kr;
+        head = false;
+        clear();
       }
 #pragma unroll
-      for (int q = 0; q < kRunIlp; ++q) {
-        if (r + q >= b) break;
-        if (kr[q] != k) {
-          done(false);
-          k = kr[q];
-          head = false;
-          clear();
-        }
-        if (j[q] >= 0)
-#pragma unroll
-          for (int i = 0; i < V; ++i) sum[i] += to_f(x[q].x[i]);
-      }
+      for (int i = 0; i < V; ++i) sum[i] += to_f(x.x[i]);
     }
     start = whole = false;  // of the last run: the first may have left a slot 0
-    done(b < n && key_at(b) == k);
+    done(k == (b < m ? s_key[b] : after));
     if (tv == 0) {
       s_start[team] = start;
       s_whole[team] = whole;
@@ -684,50 +709,42 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   __syncthreads();
   if (!on) return;
   // runs that came into the block (team 0), and that start in this team
-  bool used0 = false, used1 = false;
+  bool used0 = false;
   const auto leave = [&](int slot, uint32_t key, bool zero) {
     const int64_t p = 2 * blk + slot;
     if (c == 0) pkey[p] = key;
 #pragma unroll
     for (int i = 0; i < V; ++i) psum[p * ldp + c + i] = zero ? 0.f : sum[i];
-    (slot ? used1 : used0) = true;
   };
   const auto add_following = [&](int u) {  // -> true if the run leaves the block
     for (; u < used; ++u) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += s_part[0][(u * width + tv) * V + i];
+      for (int i = 0; i < V; ++i) sum[i] += s_part[(u * width + tv) * V + i];
       if (!s_whole[u]) return false;
     }
     return true;
   };
   const auto load = [&](int slot) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = s_part[slot][t * V + i];
+    for (int i = 0; i < V; ++i) sum[i] = s_part[slot * kThreads * V + t * V + i];
   };
-  if (team == 0 && A > 0) {
-    const uint32_t first = key_at(A);
-    if (first != kNoRow && key_at(A - 1) == first) {
-      load(0);
-      const bool through = s_whole[0] && add_following(1);
-      leave(0, first, false);
-      if (through) leave(1, first, true);
-    }
+  if (team == 0 && before != kNoRow && before == s_key[0]) {
+    load(0);
+    const bool through = s_whole[0] && add_following(1);
+    leave(0, before, false);
+    if (through) leave(1, before, true);
+    used0 = true;
   }
-  bool tail = false;
   if (s_start[team]) {
     load(1);
-    tail = add_following(team + 1);
-    if (tail) leave(1, k, false);
+    if (add_following(team + 1)) leave(1, k, false);
     else to_table(k);
   }
   // the partials that nothing set: entry 0 is team 0's, entry 1 whoever's run
   // leaves the block
   if (c == 0) {
     if (team == 0 && !used0) pkey[2 * blk] = kNoRow;
-    if (team == used - 1) {
-      const uint32_t last = key_at(B - 1);
-      if (last == kNoRow || B == n || key_at(B) != last) pkey[2 * blk + 1] = kNoRow;
-    }
+    if (team == used - 1 && (after == kNoRow || after != s_key[m - 1])) pkey[2 * blk + 1] = kNoRow;
   }
 }
 
@@ -925,20 +942,21 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   Carver cv(ws, cap);
   w.ldp = (cols + 7) / 8 * 8;
   const Passes ps(rows);
-  w.pairs[0] = cv.take<uint2>(round_up(n, kRunIlp));
+  w.pairs[0] = cv.take<uint2>(n);
   w.pairs[1] = cv.take<uint2>(n);
   w.counts = cv.take<uint32_t>(((size_t)1 << ps.bits) * ((n + kSortTile - 1) / kSortTile));
   w.total = cv.take<uint32_t>((size_t)1 << ps.bits);
-  // partials: the most that any vector width leaves (the narrowest teams)
+  // partials: the most that any type and alignment leaves
   int64_t m = n;
   for (int k = 0; k < 2; ++k) {
-    int64_t most = 0;
-    for (int V = 1; V <= 8; V *= 2) {
-      const int64_t b = RunShape(m, cols, V, k ? kRunIlp : 0).blocks;
-      if (b > most) most = b;
-    }
+    int64_t most = k ? RunShape(m, cols, 4, 4, false).blocks : 0;
+    for (int es = 2; !k && es <= 4; es += 2)
+      for (int V = 1; V <= 16 / es; V += 16 / es - 1) {
+        const int64_t b = RunShape(m, cols, V, es, true).blocks;
+        if (b > most) most = b;
+      }
     m = 2 * most;
-    w.pkey[k] = cv.take<uint32_t>(round_up(m, kRunIlp));
+    w.pkey[k] = cv.take<uint32_t>(m);
     w.psum[k] = cv.take<float>((size_t)m * w.ldp);
   }
   if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
@@ -989,25 +1007,35 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
   return GS_OK;
 }
 
+template <class T, int V, bool FIRST>
+gs_status launch_sums(const uint2* pairs, const uint32_t* keys, int64_t n, const RunShape& sh,
+                      const T* g, int64_t rs, int cols, float scale, float* dt, int64_t ld,
+                      bool accumulate, uint32_t* pkey, float* psum, int ldp, cudaStream_t s) {
+  if (sh.blocks * sh.col_tiles > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
+  static std::atomic<unsigned long long> once{0};
+  GS_TRY(smem_attrs_once((const void*)k_run_sums<T, V, FIRST>,
+                         kRunRowBytes + 2 * kThreads * V * 4 + kRunEntries * 8, &once));
+  GS_TRY(launch_dependent(k_run_sums<T, V, FIRST>, (unsigned)(sh.blocks * sh.col_tiles), kThreads,
+                          sh.smem, s, pairs, keys, n, sh, g, rs, cols, scale, dt, ld, accumulate,
+                          pkey, psum, ldp));
+  GS_LAUNCH_CHECK();
+  return GS_OK;
+}
+
 template <class T, int V>
 gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, float* dt, int64_t ld,
                    bool accumulate, const LookupWs& w, cudaStream_t s) {
-  RunShape sh(n, cols, V, 0);
-  if (sh.blocks * sh.col_tiles > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
-  GS_TRY(launch_dependent(k_run_sums<T, V, true>, (unsigned)(sh.blocks * sh.col_tiles), sh.threads, 0,
-                          s, w.pairs[0], nullptr, n, sh.len, sh.teams, sh.width, sh.col_tiles, g, rs,
-                          cols, scale, dt, ld, accumulate, w.pkey[0], w.psum[0], w.ldp));
-  GS_LAUNCH_CHECK();
-  for (int from = 0; sh.blocks > 1; from ^= 1) {
+  RunShape sh(n, cols, V, sizeof(T), true);
+  gs_status st = launch_sums<T, V, true>(w.pairs[0], nullptr, n, sh, g, rs, cols, scale, dt, ld,
+                                         accumulate, w.pkey[0], w.psum[0], w.ldp, s);
+  for (int from = 0; st == GS_OK && sh.blocks > 1; from ^= 1) {
     const int64_t m = 2 * sh.blocks;
-    sh = RunShape(m, cols, 4, kRunIlp);
-    GS_TRY(launch_dependent(k_run_sums<float, 4, false>, (unsigned)(sh.blocks * sh.col_tiles),
-                            sh.threads, 0, s, nullptr, w.pkey[from], m, sh.len, sh.teams, sh.width,
-                            sh.col_tiles, w.psum[from], w.ldp, cols, scale, dt, ld, accumulate,
-                            w.pkey[from ^ 1], w.psum[from ^ 1], w.ldp));
-    GS_LAUNCH_CHECK();
+    sh = RunShape(m, cols, 4, 4, false);
+    st = launch_sums<float, 4, false>(nullptr, w.pkey[from], m, sh, w.psum[from], w.ldp, cols, scale,
+                                      dt, ld, accumulate, w.pkey[from ^ 1], w.psum[from ^ 1], w.ldp,
+                                      s);
   }
-  return GS_OK;
+  return st;
 }
 
 // Elements of size es that may move together: a divisor of cols and the
