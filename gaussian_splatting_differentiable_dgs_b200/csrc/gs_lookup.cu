@@ -589,8 +589,8 @@ struct RunShape {
     width = (nv + col_tiles - 1) / col_tiles;
     pitch = V == 1 ? (width * es + 3) / 4 * 4 : 16 * (width | 1);
     teams = kThreads / width < kMaxTeams ? kThreads / width : kMaxTeams;
-    // what fits, for the items no more than leaves eight blocks for each SM
-    int64_t e = kRunRowBytes / pitch, fill = n / (148 * 8);
+    // what fits, for the items no more than leaves two blocks for each SM
+    int64_t e = kRunRowBytes / pitch, fill = n / (148 * 2);
     if (e > kRunEntries) e = kRunEntries;
     if (first && e > fill) e = fill < 64 ? 64 : fill;
     entries = (int)e;
@@ -912,11 +912,158 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
   }
 }
 
+// Tables that fit in shared memory, a few columns at a time, need no sort: a
+// block owns up to 4 * kPrivWarps columns of a table of its own and a split of
+// the items, a warp four of the columns.  The warp adds 32 items at a time in
+// order: lanes with the same id first sum their values by pointer jumping
+// along the lanes (log2 of the largest group's steps, none if all ids
+// differ), then each group's first lane adds to the table.  The groups are
+// found once for all columns.  g is read once, as it lies (planes are
+// coalesced); the splits' tables are summed by k_join_tables in order.
+constexpr int kPrivWarps = 8, kPrivTile = 256, kPrivBytes = 96 * 1024;
+
+struct PrivShape {
+  int warps, cols, col_groups;  // columns per block
+  int64_t splits, per;          // items per split
+  size_t smem, partial;         // bytes
+  bool use;
+  PrivShape(int64_t n, int64_t rows, int all) : use(false) {
+    if (n <= kSmallItems || rows > kPrivBytes / 16) return;
+    use = true;
+    int64_t c = kPrivBytes / (4 * rows) / 4 * 4;
+    if (c > 4 * kPrivWarps) c = 4 * kPrivWarps;
+    col_groups = (int)((all + c - 1) / c);
+    cols = ((all + col_groups - 1) / col_groups + 3) / 4 * 4;
+    col_groups = (all + cols - 1) / cols;
+    warps = cols / 4;
+    smem = (size_t)rows * cols * 4;
+    // blocks for the device, whose tables are at most half the items' size
+    int64_t at_once = (int64_t)(220 * 1024 / (smem + 6 * 1024));
+    if (at_once > 8) at_once = 8;
+    splits = 148 * at_once / col_groups;
+    if (splits > n / (2 * rows)) splits = n / (2 * rows);
+    if (splits > n / kPrivTile) splits = n / kPrivTile;
+    if (splits < 1) splits = 1;
+    per = ((n + splits - 1) / splits + kPrivTile - 1) / kPrivTile * kPrivTile;
+    splits = (n + per - 1) / per;
+    partial = (size_t)splits * all * rows * 4;
+  }
+};
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(32 * kPrivWarps)
+k_private_sums(const T* __restrict__ g, int64_t rs, int64_t cs, int all,
+               const __grid_constant__ Ids src, int64_t n, int64_t per, int64_t splits, int cols,
+               float* __restrict__ partial, int32_t* dev_status) {
+  constexpr int GROUPS = kPrivTile / 32;
+  extern __shared__ __align__(16) float s_table[];  // [cols][rows]
+  __shared__ int32_t s_id[2][kPrivTile];
+  __shared__ uint32_t s_mask[2][kPrivTile];
+  __shared__ int s_steps[2][GROUPS];
+  wait_for_prior_grids();
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5, threads = blockDim.x;
+  const int rows = (int)src.rows;
+  const int64_t split = blockIdx.x % splits;
+  const int c0 = (int)(blockIdx.x / splits) * cols + 4 * w;  // this warp's first column
+  const int64_t first = split * per, last = min(first + per, n);
+  for (int i = t; i < cols * rows; i += threads) s_table[i] = 0.f;
+  float* table = s_table + 4 * w * rows;
+  const uint32_t below = (1u << lane) - 1;
+  int buf = 0;
+  for (int64_t j0 = first; j0 < last; j0 += kPrivTile, buf ^= 1) {
+    for (int i = t; i < kPrivTile; i += threads) {
+      const int64_t j = j0 + i;
+      const int32_t id =
+          j < last ? id_of(src.ids, src.n_ids, src.index, j, src.rows, dev_status) : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      const uint32_t mask = id >= 0 ? same : 1u << lane;
+      const int most = __reduce_max_sync(0xffffffffu, __popc(mask));
+      s_id[buf][i] = id;
+      s_mask[buf][i] = mask;
+      if (lane == 0) s_steps[buf][i >> 5] = 32 - __clz(most - 1);  // ceil(log2(most))
+    }
+    Pack<T, 4> x[GROUPS];
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      const int64_t j = j0 + k * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k].x[i] = from_f<T>(0.f);
+      if (j >= last) continue;
+      const T* p = g + j * rs + (int64_t)c0 * cs;
+      if (VEC) {
+        if (c0 < all) x[k] = *reinterpret_cast<const Pack<T, 4>*>(p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i < all) x[k].x[i] = p[i * cs];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      const int32_t id = s_id[buf][k * 32 + lane];
+      const uint32_t mask = s_mask[buf][k * 32 + lane];
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = to_f(x[k].x[i]);
+      const uint32_t above = mask & ~below & ~(1u << lane);
+      int next = above ? __ffs(above) - 1 : 32;  // the group's next lane; 32: none
+      for (int steps = s_steps[buf][k]; steps > 0; --steps) {
+        const int from = next & 31, jump = __shfl_sync(0xffffffffu, next, from);
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, v[i], from);
+        if (next < 32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += y[i];
+          next = jump;
+        }
+      }
+      if (id >= 0 && !(mask & below)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) table[i * rows + id] += v[i];
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  const int from = (int)(blockIdx.x / splits) * cols, width = min(cols, all - from);
+  float* o = partial + (split * all + from) * rows;
+  for (int i = t; i < width * rows; i += threads) o[i] = s_table[i];
+}
+
+// dtable[k][c] (+)= scale * sum of partial[split][c][k] over the splits, eight
+// stretches of them at a time.
+__global__ void __launch_bounds__(kThreads)
+k_join_tables(const float* __restrict__ partial, int64_t splits, int cols, int rows, float scale,
+              float* __restrict__ dtable, int64_t ld, bool accumulate) {
+  constexpr int PARTS = kThreads / 32;
+  __shared__ float s_sum[PARTS][32];
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t total = (int64_t)cols * rows, e = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t each = (splits + PARTS - 1) / PARTS, a = w * each, b = min(a + each, splits);
+  float sum = 0.f;
+  if (e < total) {
+    const float* p = partial + e;
+#pragma unroll 8
+    for (int64_t i = a; i < b; ++i) sum += p[i * total];
+  }
+  s_sum[w][lane] = sum;
+  __syncthreads();
+  if (w == 0 && e < total) {
+    for (int k = 1; k < PARTS; ++k) sum += s_sum[k][lane];
+    float* d = dtable + e % rows * ld + e / rows;
+    *d = accumulate ? *d + scale * sum : scale * sum;
+  }
+}
+
 unsigned blocks_for(int64_t threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
 
 int key_bits(int64_t rows) { return rows > 1 ? 64 - __builtin_clzll((unsigned long long)(rows - 1)) : 0; }
 
 struct LookupWs {
+  float* partial;   // private tables
   uint2* pairs[2];  // the sorted order ends in pairs[0]
   uint32_t* counts;
   uint32_t* total;
@@ -940,6 +1087,12 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   LookupWs w{};
   if (n <= kSmallItems) return w;
   Carver cv(ws, cap);
+  const PrivShape priv(n, rows, cols);
+  if (priv.use) {
+    w.partial = cv.take<float>(priv.partial / 4);
+    w.bytes = cv.off;
+    return w;
+  }
   w.ldp = (cols + 7) / 8 * 8;
   const Passes ps(rows);
   w.pairs[0] = cv.take<uint2>(n);
@@ -1146,7 +1299,7 @@ extern "C" size_t gs_lookup_bwd_workspace_size(int64_t n, int64_t rows, int32_t 
                                                int32_t planes) {
   if (n < 0 || n > (int64_t)INT32_MAX || rows < 1 || rows > (int64_t)INT32_MAX || cols < 1) return 0;
   const size_t b = carve_lookup(nullptr, 0, n, rows, cols, planes ? 4 : 0).bytes;
-  return b ? b : 256;
+  return b > 256 ? b : 256;
 }
 
 extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int32_t* index,
@@ -1159,7 +1312,7 @@ extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int
   const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, cols, 0);
   if (!ws || w.bytes > ws_bytes || ws_bytes < 256) return GS_ERR_CAPACITY;
   if (!aligned(ws, 256)) return GS_ERR_ARG;
-  if (n <= kSmallItems) return GS_OK;  // such gradients need no order
+  if (!w.pairs[0]) return GS_OK;  // such gradients need no order
   return plan_lookup(ids, n_ids, index, n, rows, w, nullptr, 0, dev_status, to_stream(stream));
 }
 
@@ -1186,6 +1339,30 @@ gs_status small_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, cons
 }
 
 template <class T>
+gs_status private_grad(const gs_matrix* g, const Ids& src, float scale, const gs_matrix* dtable,
+                       bool accumulate, const PrivShape& ps, float* partial, int32_t* dev_status,
+                       cudaStream_t s) {
+  const T* data = static_cast<const T*>(g->data);
+  const bool vec = g->col_stride == 1 &&
+                   vector_of(data, g->row_stride, g->cols, sizeof(T), 4) == 4;
+  const auto kernel = vec ? k_private_sums<T, true> : k_private_sums<T, false>;
+  const int64_t join = ((int64_t)g->cols * src.rows + 31) / 32;
+  if (join > (int64_t)INT32_MAX || ps.splits * ps.col_groups > (int64_t)INT32_MAX)
+    return GS_ERR_UNSUPPORTED;
+  static std::atomic<unsigned long long> once[2];
+  GS_TRY(smem_attrs_once((const void*)kernel, kPrivBytes, &once[vec]));
+  GS_TRY(launch_dependent(kernel, (unsigned)(ps.splits * ps.col_groups), 32 * ps.warps, ps.smem, s,
+                          data, g->row_stride, g->col_stride, g->cols, src, g->rows, ps.per,
+                          ps.splits, ps.cols, partial, dev_status));
+  GS_LAUNCH_CHECK();
+  const int rows = (int)src.rows;
+  GS_TRY(launch_dependent(k_join_tables, (unsigned)join, kThreads, 0, s, partial, ps.splits, g->cols, rows, scale,
+                          static_cast<float*>(dtable->data), dtable->row_stride, accumulate));
+  GS_LAUNCH_CHECK();
+  return GS_OK;
+}
+
+template <class T>
 gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, const int32_t* index,
                       float scale, const gs_matrix* dtable, bool accumulate, const LookupWs& w,
                       int32_t* dev_status, cudaStream_t s) {
@@ -1198,6 +1375,10 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
   if (n <= kSmallItems)
     return vec ? small_grad<T, V>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s)
                : small_grad<T, 1>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s);
+  const PrivShape ps(n, dtable->rows, cols);
+  if (ps.use)
+    return private_grad<T>(g, Ids{ids, index, n_ids, dtable->rows}, scale, dtable, accumulate, ps,
+                           w.partial, dev_status, s);
   float* dt = static_cast<float*>(dtable->data);
   const int64_t ld = dtable->row_stride;
   if (planes) {
@@ -1236,14 +1417,15 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
     if (!aligned(ws, 256)) return GS_ERR_ARG;
   }
   const bool accumulate = (flags & GS_LOOKUP_ACCUMULATE) != 0;
-  const bool plan = !(flags & GS_LOOKUP_PLANNED) && n > kSmallItems;
+  const bool sorted = n > kSmallItems && !PrivShape(n, rows, g->cols).use;
+  const bool plan = !(flags & GS_LOOKUP_PLANNED) && sorted;
   float* dt = static_cast<float*>(dtable->data);
   // rows that no item uses: cleared by the sort's first kernel where the table
   // is contiguous and no block of it gets more than 32 KB to clear
   const int64_t elements = rows * dtable->cols, tiles = (n + kSortTile - 1) / kSortTile;
   const bool fused = plan && !accumulate && dtable->row_stride == dtable->cols &&
                      elements <= tiles * 8192;
-  if (!accumulate && !fused && (n == 0 || n > kSmallItems))
+  if (!accumulate && !fused && (n == 0 || sorted))
     GS_TRY(cudaMemset2DAsync(dt, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
   if (n == 0) return GS_OK;
   if (plan) {

@@ -618,8 +618,8 @@ gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
  *   dtable[k][c] = scale * sum over {j : id_j = k} of g[j][c]
  * (+= with GS_LOOKUP_ACCUMULATE), fp32, rows contiguous; rows of the table
  * that no item uses get zero.  Items with id_j < 0 or out of range add
- * nothing (their g is not read).  The items are sorted by id and summed in
- * fp32 in a fixed order: equal inputs give equal bits.  At most 2^31 - 1
+ * nothing, whatever their g holds.  The sums are fp32 sums in a fixed order:
+ * equal inputs give equal bits.  At most 2^31 - 1
  * items and rows.
  * ws: gs_lookup_bwd_workspace_size(n, rows, cols) bytes, planes: whether g is
  * in planes (col_stride other than 1).  gs_lookup_plan writes the
