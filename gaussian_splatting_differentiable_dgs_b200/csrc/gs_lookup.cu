@@ -912,24 +912,29 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
   }
 }
 
-// Tables that fit in shared memory, a few columns at a time, need no sort: a
-// block owns up to 4 * kPrivWarps columns of a table of its own and a split of
-// the items, a warp four of the columns.  The warp adds 32 items at a time in
-// order: lanes with the same id first sum their values by pointer jumping
-// along the lanes (log2 of the largest group's steps, none if all ids
-// differ), then each group's first lane adds to the table.  The groups are
-// found once for all columns.  g is read once, as it lies (planes are
-// coalesced); the splits' tables are summed by k_join_tables in order.
-constexpr int kPrivWarps = 8, kPrivTile = 256, kPrivBytes = 96 * 1024;
+// A gradient in planes for a table of at most kPrivRows rows needs no sort and
+// no turning: a block owns up to 4 * kPrivWarps columns of a table of its own
+// in shared memory and a split of the items, a warp four of the columns.  The
+// warp adds 32 items at a time in order: lanes with the same id first sum
+// their values by pointer jumping along the lanes (log2 of the largest
+// group's steps, none if all ids differ), then each group's first lane adds
+// to the table.  The groups are found once for all columns.  g is read once,
+// as it lies; the splits' tables are summed by k_join_tables in order.
+// Bound by instruction issue and the shared memory's latency: 2.5M x 48 for
+// 1024 rows take 262 us against 367 by the sort, 150K x 12 take 23 against
+// 44; at 2048 rows, with half the columns per block, it is 441 against 361.
+// For a gradient in rows the sort is faster at any size (300K x 128 for 1000
+// rows: 75 us against 157).
+constexpr int kPrivRows = 1024, kPrivWarps = 8, kPrivTile = 256, kPrivBytes = 96 * 1024;
 
 struct PrivShape {
   int warps, cols, col_groups;  // columns per block
   int64_t splits, per;          // items per split
   size_t smem, partial;         // bytes
   bool use;
-  PrivShape(int64_t n, int64_t rows, int all) : use(false) {
-    if (n <= kSmallItems || rows > kPrivBytes / 16) return;
-    use = true;
+  PrivShape(int64_t n, int64_t rows, int all, bool planes)
+      : use(planes && n > kSmallItems && rows <= kPrivRows) {
+    if (!use) return;
     int64_t c = kPrivBytes / (4 * rows) / 4 * 4;
     if (c > 4 * kPrivWarps) c = 4 * kPrivWarps;
     col_groups = (int)((all + c - 1) / c);
@@ -937,12 +942,14 @@ struct PrivShape {
     col_groups = (all + cols - 1) / cols;
     warps = cols / 4;
     smem = (size_t)rows * cols * 4;
-    // blocks for the device, whose tables are at most half the items' size
+    // blocks for the device, of two tiles or more, whose tables are at most as
+    // large as the items or stay in L2
     int64_t at_once = (int64_t)(220 * 1024 / (smem + 6 * 1024));
     if (at_once > 8) at_once = 8;
     splits = 148 * at_once / col_groups;
-    if (splits > n / (2 * rows)) splits = n / (2 * rows);
-    if (splits > n / kPrivTile) splits = n / kPrivTile;
+    const int64_t table = rows * all * 4, most = n / rows > (16 << 20) / table ? n / rows : (16 << 20) / table;
+    if (splits > most) splits = most;
+    if (splits > n / (2 * kPrivTile)) splits = n / (2 * kPrivTile);
     if (splits < 1) splits = 1;
     per = ((n + splits - 1) / splits + kPrivTile - 1) / kPrivTile * kPrivTile;
     splits = (n + per - 1) / per;
@@ -950,13 +957,13 @@ struct PrivShape {
   }
 };
 
-template <class T, bool VEC>
+template <class T>
 __global__ void __launch_bounds__(32 * kPrivWarps)
-k_private_sums(const T* __restrict__ g, int64_t rs, int64_t cs, int all,
+k_private_sums(const T* __restrict__ g, int64_t cs, int all,
                const __grid_constant__ Ids src, int64_t n, int64_t per, int64_t splits, int cols,
                float* __restrict__ partial, int32_t* dev_status) {
   constexpr int GROUPS = kPrivTile / 32;
-  extern __shared__ __align__(16) float s_table[];  // [cols][rows]
+  extern __shared__ __align__(16) float s_table[];  // [warp][rows][4]
   __shared__ int32_t s_id[2][kPrivTile];
   __shared__ uint32_t s_mask[2][kPrivTile];
   __shared__ int s_steps[2][GROUPS];
@@ -967,37 +974,48 @@ k_private_sums(const T* __restrict__ g, int64_t rs, int64_t cs, int all,
   const int c0 = (int)(blockIdx.x / splits) * cols + 4 * w;  // this warp's first column
   const int64_t first = split * per, last = min(first + per, n);
   for (int i = t; i < cols * rows; i += threads) s_table[i] = 0.f;
-  float* table = s_table + 4 * w * rows;
+  float4* table = reinterpret_cast<float4*>(s_table) + w * rows;
   const uint32_t below = (1u << lane) - 1;
   int buf = 0;
+  const T* col[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) col[i] = g + (int64_t)min(c0 + i, all - 1) * cs;
+  // the ids of a tile are fetched while the tile before is summed
+  int32_t ids[GROUPS];
+  const auto fetch_ids = [&](int64_t j0) {
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+      const int64_t j = j0 + t + q * threads;
+      ids[q] = t + q * threads < kPrivTile && j < last
+                   ? id_of(src.ids, src.n_ids, src.index, j, src.rows, dev_status)
+                   : -1;
+    }
+  };
+  fetch_ids(first);
   for (int64_t j0 = first; j0 < last; j0 += kPrivTile, buf ^= 1) {
-    for (int i = t; i < kPrivTile; i += threads) {
-      const int64_t j = j0 + i;
-      const int32_t id =
-          j < last ? id_of(src.ids, src.n_ids, src.index, j, src.rows, dev_status) : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, id);
-      const uint32_t mask = id >= 0 ? same : 1u << lane;
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+      const int i = t + q * threads;
+      if (i >= kPrivTile) break;  // whole warps: threads and the tile are multiples of 32
+      const uint32_t same = __match_any_sync(0xffffffffu, ids[q]);
+      const uint32_t mask = ids[q] >= 0 ? same : 1u << lane;
       const int most = __reduce_max_sync(0xffffffffu, __popc(mask));
-      s_id[buf][i] = id;
+      s_id[buf][i] = ids[q];
       s_mask[buf][i] = mask;
       if (lane == 0) s_steps[buf][i >> 5] = 32 - __clz(most - 1);  // ceil(log2(most))
     }
+    // rows and columns that do not exist are read at the last ones and not used
     Pack<T, 4> x[GROUPS];
+    const auto fetch_rows = [&](auto at) {  // at(k): item of this lane in group k
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) {
-      const int64_t j = j0 + k * 32 + lane;
+      for (int k = 0; k < GROUPS; ++k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[k].x[i] = from_f<T>(0.f);
-      if (j >= last) continue;
-      const T* p = g + j * rs + (int64_t)c0 * cs;
-      if (VEC) {
-        if (c0 < all) x[k] = *reinterpret_cast<const Pack<T, 4>*>(p);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c0 + i < all) x[k].x[i] = p[i * cs];
+        for (int i = 0; i < 4; ++i) x[k].x[i] = col[i][at(k)];
       }
-    }
+    };
+    if (j0 + kPrivTile <= last) fetch_rows([&](int k) { return j0 + lane + k * 32; });
+    else fetch_rows([&](int k) { return min(j0 + lane + k * 32, last - 1); });
+    if (j0 + kPrivTile < last) fetch_ids(j0 + kPrivTile);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < GROUPS; ++k) {
@@ -1006,22 +1024,26 @@ k_private_sums(const T* __restrict__ g, int64_t rs, int64_t cs, int all,
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = to_f(x[k].x[i]);
-      const uint32_t above = mask & ~below & ~(1u << lane);
-      int next = above ? __ffs(above) - 1 : 32;  // the group's next lane; 32: none
-      for (int steps = s_steps[buf][k]; steps > 0; --steps) {
-        const int from = next & 31, jump = __shfl_sync(0xffffffffu, next, from);
-        float y[4];
+      int steps = s_steps[buf][k];
+      if (steps > 0) {
+        const uint32_t above = mask & ~below & ~(1u << lane);
+        int next = above ? __ffs(above) - 1 : 32;  // the group's next lane; 32: none
+        do {
+          const int from = next & 31, jump = __shfl_sync(0xffffffffu, next, from);
+          float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, v[i], from);
-        if (next < 32) {
+          for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, v[i], from);
+          if (next < 32) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += y[i];
-          next = jump;
-        }
+            for (int i = 0; i < 4; ++i) v[i] += y[i];
+            next = jump;
+          }
+        } while (--steps > 0);
       }
       if (id >= 0 && !(mask & below)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) table[i * rows + id] += v[i];
+        float4 y = table[id];
+        y.x += v[0], y.y += v[1], y.z += v[2], y.w += v[3];
+        table[id] = y;
       }
       __syncwarp();
     }
@@ -1029,7 +1051,8 @@ k_private_sums(const T* __restrict__ g, int64_t rs, int64_t cs, int all,
   __syncthreads();
   const int from = (int)(blockIdx.x / splits) * cols, width = min(cols, all - from);
   float* o = partial + (split * all + from) * rows;
-  for (int i = t; i < width * rows; i += threads) o[i] = s_table[i];
+  for (int c = 0; c < width; ++c, o += rows)
+    for (int k = t; k < rows; k += threads) o[k] = s_table[((c >> 2) * rows + k) * 4 + (c & 3)];
 }
 
 // dtable[k][c] (+)= scale * sum of partial[split][c][k] over the splits, eight
@@ -1087,12 +1110,6 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   LookupWs w{};
   if (n <= kSmallItems) return w;
   Carver cv(ws, cap);
-  const PrivShape priv(n, rows, cols);
-  if (priv.use) {
-    w.partial = cv.take<float>(priv.partial / 4);
-    w.bytes = cv.off;
-    return w;
-  }
   w.ldp = (cols + 7) / 8 * 8;
   const Passes ps(rows);
   w.pairs[0] = cv.take<uint2>(n);
@@ -1112,7 +1129,10 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
     w.pkey[k] = cv.take<uint32_t>(m);
     w.psum[k] = cv.take<float>((size_t)m * w.ldp);
   }
-  if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
+  // behind what a kept order needs
+  const PrivShape priv(n, rows, cols, planes_es != 0);
+  if (priv.use) w.partial = cv.take<float>(priv.partial / 4);
+  else if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
   w.bytes = cv.off;
   return w;
 }
@@ -1342,18 +1362,14 @@ template <class T>
 gs_status private_grad(const gs_matrix* g, const Ids& src, float scale, const gs_matrix* dtable,
                        bool accumulate, const PrivShape& ps, float* partial, int32_t* dev_status,
                        cudaStream_t s) {
-  const T* data = static_cast<const T*>(g->data);
-  const bool vec = g->col_stride == 1 &&
-                   vector_of(data, g->row_stride, g->cols, sizeof(T), 4) == 4;
-  const auto kernel = vec ? k_private_sums<T, true> : k_private_sums<T, false>;
   const int64_t join = ((int64_t)g->cols * src.rows + 31) / 32;
   if (join > (int64_t)INT32_MAX || ps.splits * ps.col_groups > (int64_t)INT32_MAX)
     return GS_ERR_UNSUPPORTED;
-  static std::atomic<unsigned long long> once[2];
-  GS_TRY(smem_attrs_once((const void*)kernel, kPrivBytes, &once[vec]));
-  GS_TRY(launch_dependent(kernel, (unsigned)(ps.splits * ps.col_groups), 32 * ps.warps, ps.smem, s,
-                          data, g->row_stride, g->col_stride, g->cols, src, g->rows, ps.per,
-                          ps.splits, ps.cols, partial, dev_status));
+  static std::atomic<unsigned long long> once{0};
+  GS_TRY(smem_attrs_once((const void*)k_private_sums<T>, kPrivBytes, &once));
+  GS_TRY(launch_dependent(k_private_sums<T>, (unsigned)(ps.splits * ps.col_groups), 32 * ps.warps,
+                          ps.smem, s, static_cast<const T*>(g->data), g->col_stride, g->cols, src,
+                          g->rows, ps.per, ps.splits, ps.cols, partial, dev_status));
   GS_LAUNCH_CHECK();
   const int rows = (int)src.rows;
   GS_TRY(launch_dependent(k_join_tables, (unsigned)join, kThreads, 0, s, partial, ps.splits, g->cols, rows, scale,
@@ -1375,7 +1391,7 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
   if (n <= kSmallItems)
     return vec ? small_grad<T, V>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s)
                : small_grad<T, 1>(g, ids, n_ids, index, scale, dtable, accumulate, dev_status, s);
-  const PrivShape ps(n, dtable->rows, cols);
+  const PrivShape ps(n, dtable->rows, cols, planes);
   if (ps.use)
     return private_grad<T>(g, Ids{ids, index, n_ids, dtable->rows}, scale, dtable, accumulate, ps,
                            w.partial, dev_status, s);
@@ -1417,7 +1433,7 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
     if (!aligned(ws, 256)) return GS_ERR_ARG;
   }
   const bool accumulate = (flags & GS_LOOKUP_ACCUMULATE) != 0;
-  const bool sorted = n > kSmallItems && !PrivShape(n, rows, g->cols).use;
+  const bool sorted = n > kSmallItems && !PrivShape(n, rows, g->cols, planes_es != 0).use;
   const bool plan = !(flags & GS_LOOKUP_PLANNED) && sorted;
   float* dt = static_cast<float*>(dtable->data);
   // rows that no item uses: cleared by the sort's first kernel where the table
