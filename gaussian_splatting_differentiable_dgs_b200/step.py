@@ -20,6 +20,7 @@ import numpy as np
 import torch
 
 from . import binding as B
+from .codebook import SH_PLANE
 
 DEFAULT_BUDGET = 384 << 20
 
@@ -211,12 +212,17 @@ class Stepper:
     three list builders), mode ("bounded" or the whole-image "original"),
     loss ("l1" or "l1_ssim" with weight ssim_lambda), leaf_streams (1: one
     Leaf at a time; k = 2..4: consecutive Leaves on k streams with k raster
-    arenas)."""
+    arenas), max_grad_norm (the view's whole gradient is scaled to at most
+    this L2 norm before Adam; `last_grad_norm` gives the norm before that),
+    codebook (codebook.ColorCodebook: the SH planes are decoded from its
+    table, and the update trains the table instead of them).  Both take the
+    view's gradient as compact 3D gradients (fuse_adam's fused pass never
+    holds the whole gradient)."""
 
     def __init__(self, model: GaussianModel, budget: int = DEFAULT_BUDGET, lr=1e-3,
                  betas=(0.9, 0.999), eps=1e-8, raster_flags=0, fuse_adam=True,
                  binning="fused", mode="bounded", loss="l1", ssim_lambda=B.SSIM_LAMBDA,
-                 leaf_streams=1, device="cuda"):
+                 leaf_streams=1, device="cuda", max_grad_norm=None, codebook=None):
         if binning not in ("fused", "expand", "sort"):
             raise ValueError(f"binning must be 'fused', 'expand' or 'sort', not {binning!r}")
         if mode not in ("bounded", "original"):
@@ -237,6 +243,14 @@ class Stepper:
         # l1: the L1 photometric loss; l1_ssim: the composite
         # (1 - lambda) L1 + lambda (1 - SSIM) of 3DGS training (SkipGS notes,
         # "loss function / training strategy"), SSIM windows local to each Leaf
+        if max_grad_norm is not None and not 0.0 <= float(max_grad_norm) < math.inf:
+            raise ValueError(f"max_grad_norm must be finite and not negative, not {max_grad_norm!r}")
+        if codebook is not None:
+            codebook.check(model)
+        self.max_grad_norm = None if max_grad_norm is None else float(max_grad_norm)
+        self.codebook = codebook
+        self._clip = None     # device {norm, coefficient}
+        self._clip_ws = None
         self.loss = loss
         self.ssim_lambda = float(ssim_lambda)
         self.mode = mode
@@ -259,6 +273,8 @@ class Stepper:
         self._after_tables = []
         self._arena_hint = 0  # bytes per Leaf arena (bounded runs), see run_view
         self._cap_hint = {}  # region -> candidate capacity for the next view
+        if codebook is not None:
+            codebook.decode(model, self.dev_status)
 
     def reserve(self, cams, region=None):
         """Sizes the Leaf arenas for the views a run will step through: each
@@ -305,6 +321,45 @@ class Stepper:
 
     def last_loss(self) -> float:
         return float(self._last_loss.item())
+
+    def last_grad_norm(self) -> float:
+        """The norm of the last update's gradient, before clipping."""
+        if self._clip is None:
+            raise ValueError("no update with max_grad_norm was taken")
+        return float(self._clip[0].item())
+
+    def _update(self, g, stride, slot, cols, cand_idx):
+        """One Adam update from the view's gradient g [P][stride] (`cols`
+        columns, of the candidates cand_idx with their slots, or of all
+        Gaussians), through the codebook and clipped as the options say."""
+        m, cb = self.model, self.codebook
+        m.step += 1
+        args = self.adam_args(m.step)
+        planes = m.P if cb is None else SH_PLANE
+        g2 = g.view(m.P, -1)[:, :cols]
+        if cb is not None:
+            cb.gradient(g2[SH_PLANE:], cand_idx, self.dev_status)
+        if self.max_grad_norm is None:
+            B.gs_adam(m.params, m.m, m.v, g, stride, slot, m.n, m.n_pad, planes, args)
+            if cb is not None:
+                size = cb.grad.numel()
+                B.gs_adam(cb.table, cb.m, cb.v, cb.grad, size, None, size, size, 1, args)
+        else:
+            grads = B.tensor_list([g2[:planes]] + ([cb.grad] if cb is not None else []))
+            if self._clip is None:
+                self._clip = torch.empty(2, dtype=torch.float32, device=self.device)
+                self._clip_ws = torch.empty(B.gs_grad_norm_workspace_size(grads),
+                                            dtype=torch.uint8, device=self.device)
+            B.gs_grad_norm(grads, self.max_grad_norm, self._clip, self._clip_ws,
+                           dev_status=self.dev_status)
+            B.gs_adam_clipped(m.params, m.m, m.v, g, stride, slot, m.n, m.n_pad, planes, args,
+                              self._clip)
+            if cb is not None:
+                size = cb.grad.numel()
+                B.gs_adam_clipped(cb.table, cb.m, cb.v, cb.grad, size, None, size, size, 1, args,
+                                  self._clip)
+        if cb is not None:
+            cb.decode(m, self.dev_status)
 
     # ------------------------------------------------------------------
     def run_view(self, cam, target, leaves=None, hooks=None, update=True, backward=True,
@@ -700,6 +755,14 @@ class Stepper:
             B.gs_grad_accumulate(g3d, max(C, 1), cand_idx, C, m.P, grad_out, m.n_pad)
             clk.toc(tk)
             del g3d
+        elif update and (self.max_grad_norm is not None or self.codebook is not None):
+            g3d = torch.empty(m.P * max(C, 1), dtype=torch.float32, device=dev)
+            tk = clk.tic("project_bwd")
+            B.gs_project_bwd(mod, camS, proj, C, g2d, g3d=g3d, g3d_stride=max(C, 1),
+                             dev_status=st)
+            self._update(g3d, max(C, 1), slot, C, cand_idx[:C])
+            clk.toc(tk)
+            del g3d
         elif update:
             m.step += 1
             if self.fuse_adam and not original:
@@ -763,10 +826,8 @@ class Stepper:
                                hooks=hooks)
             stats.append(st)
             loss = self._last_loss if loss is None else loss + self._last_loss
-        m.step += 1
         tk = _Timer(timing).tic("project_bwd")
-        B.gs_adam(m.params, m.m, m.v, self._G, m.n_pad, None, m.n, m.n_pad, m.P,
-                  self.adam_args(m.step))
+        self._update(self._G, m.n_pad, None, m.n, None)
         _Timer(timing).toc(tk)
         self._last_loss = loss
         return _merge_stats(stats)

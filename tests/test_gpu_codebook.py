@@ -1,0 +1,189 @@
+"""The view step through a colour codebook and with a clipped gradient: lookup,
+render, projection backward, the table's gradient, the norm over both and the
+clipped Adam updates, against the CPU oracle's gradient.
+
+The compact gradients are within GRAD_TOL (relative L2 per tensor) of the
+oracle's, as in the other parity tests; what follows from them here in fp64
+keeps that: the norm moves by at most GRAD_TOL of itself, a clipped gradient
+by twice that (its own error and the coefficient's), and a sum of up to m
+rows by sqrt(m) times their L2 error (Cauchy-Schwarz)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gaussian_splatting_differentiable_dgs_b200 import synth
+from gpu_util import need_gpu, rel_l2
+
+pytestmark = pytest.mark.gpu
+
+GRAD_TOL = 1e-4
+B1, B2 = 0.9, 0.999
+GROUPS = [(0, 3), (3, 6), (6, 10), (10, 11), (11, None)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+    torch.cuda.set_device(0)
+
+
+def scene(n=300, seed=9):
+    s, cams = synth.tiny_scene(n=n, width=160, height=120, sh_degree=3, seed=seed, scale_px=(1.0, 12.0))
+    return s, cams
+
+
+def oracle(oracle_mod, sc, params, cam, target):
+    return oracle_mod.step(params.astype(np.float64), sc.n, sc.sh_degree, cam, target.astype(np.float64))
+
+
+def codebook_scene(K=20, scale=0.75, seed=3):
+    """A scene whose SH planes are decoded from a table; a few without code."""
+    sc, cams = scene()
+    rng = np.random.default_rng(seed)
+    table = (rng.normal(size=(K, sc.P - 11)) * 0.2).astype(np.float32)
+    codes = rng.integers(0, K, sc.n).astype(np.int32)
+    codes[rng.random(sc.n) < 0.05] = -1
+    params = sc.params.copy()
+    decoded = np.where(codes[:, None] >= 0, np.float32(scale) * table[np.maximum(codes, 0)], np.float32(0))
+    params[11:, :sc.n] = decoded.T
+    return sc, cams, params, table, codes
+
+
+def table_grad(grad_sh, codes, K, scale):
+    out = np.zeros((K, grad_sh.shape[0]))
+    ok = codes >= 0
+    np.add.at(out, codes[ok], scale * grad_sh.T[ok])
+    return out
+
+
+def check_m(m, ref, coef, tol):
+    """Adam's first moment after one step is (1 - b1) c g; `implied` has its
+    three fp32 roundings, within 1e-6 of itself."""
+    for a, e in GROUPS:
+        e = ref.shape[0] if e is None else e
+        if e > a and np.linalg.norm(ref[a:e]) > 0:
+            assert rel_l2(m[a:e].astype(np.float64) / (1 - B1), coef * ref[a:e]) <= tol + 1e-6, (a, e)
+
+
+@pytest.mark.parametrize("share", [0.25, 50.0])
+@pytest.mark.parametrize("mode", ["bounded", "original"])
+def test_clipped_step(oracle_mod, share, mode):
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams = scene()
+    target = synth.random_image(160, 120, 12) * 0.6
+    ref = oracle(oracle_mod, sc, sc.params, cams[0], target)
+    g = ref["grad"][:, :sc.n]
+    norm = np.linalg.norm(g)
+    model = GaussianModel(sc.params, sc.n, sc.sh_degree)
+    stp = Stepper(model, budget=200_000, mode=mode, max_grad_norm=share * norm)
+    stp.run_view(cams[0], torch.as_tensor(target).cuda())
+    stp.check()
+    assert abs(stp.last_grad_norm() - norm) <= (GRAD_TOL + 1e-6) * norm
+    coef = min(1.0, share * norm / (norm + 1e-6))
+    check_m(model.m.cpu().numpy()[:, :sc.n], g, coef, 2 * GRAD_TOL)
+    # parameters after the first update move by lr where the gradient is clear
+    d = np.abs(model.params.cpu().numpy()[:, :sc.n] - ref["params"][:, :sc.n])
+    assert d[np.abs(coef * g) > 1e-3 * np.abs(coef * g).max()].max() <= 2e-5
+
+
+@pytest.mark.parametrize("max_norm", [None, 0.25, 50.0])
+def test_codebook_step(oracle_mod, max_norm):
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    scale = 0.75
+    sc, cams, params, table, codes = codebook_scene(scale=scale)
+    target = synth.random_image(160, 120, 5) * 0.6
+    ref = oracle(oracle_mod, sc, params, cams[0], target)
+    g = ref["grad"][:, :sc.n]
+    want = table_grad(g[11:], codes, len(table), scale)
+    norm = math.hypot(np.linalg.norm(g[:11]), np.linalg.norm(want))
+    model = GaussianModel(sc.params, sc.n, sc.sh_degree)  # its own colours are replaced
+    cb = ColorCodebook(table, codes, scale)
+    stp = Stepper(model, budget=200_000, codebook=cb,
+                  max_grad_norm=None if max_norm is None else max_norm * norm)
+    assert np.array_equal(model.params.cpu().numpy()[11:, :sc.n], params[11:, :sc.n])
+    stp.run_view(cams[0], torch.as_tensor(target).cuda())
+    stp.check()
+    assert abs(stp.last_loss() - ref["loss"]) <= 1e-5 * ref["loss"]
+    coef = 1.0 if max_norm is None else min(1.0, max_norm * norm / (norm + 1e-6))
+    most = np.bincount(codes[codes >= 0]).max()
+    slack = scale * math.sqrt(most) * GRAD_TOL * np.linalg.norm(g[11:])
+    got = cb.grad.cpu().numpy().astype(np.float64)
+    assert np.linalg.norm(got - want) <= slack + 1e-6 * np.linalg.norm(want)
+    tol = GRAD_TOL + slack / np.linalg.norm(want)
+    if max_norm is not None:
+        assert abs(stp.last_grad_norm() - norm) <= (tol + 1e-6) * norm
+    check_m(model.m.cpu().numpy()[:11, :sc.n], g[:11], coef, 2 * tol)
+    got_m = cb.m.cpu().numpy().astype(np.float64) / (1 - B1)
+    assert rel_l2(got_m, coef * want) <= 2 * tol + 1e-6
+    # the SH planes take no update of their own: they are the new table's rows
+    assert not model.m[11:].any() and not model.v[11:].any()
+    new = cb.table.cpu().numpy()
+    assert not np.array_equal(new, table)
+    decoded = np.where(codes[:, None] >= 0, np.float32(scale) * new[np.maximum(codes, 0)], np.float32(0))
+    assert np.array_equal(model.params.cpu().numpy()[11:, :sc.n], decoded.T)
+
+
+def test_grouped_codebook_step_matches_the_whole_view():
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams, params, table, codes = codebook_scene()
+    target = torch.as_tensor(synth.random_image(160, 120, 6) * 0.6).cuda()
+    out = []
+    for grouped in (False, True):
+        model, cb = GaussianModel(params, sc.n, sc.sh_degree), ColorCodebook(table, codes, 0.75)
+        stp = Stepper(model, budget=200_000, codebook=cb, max_grad_norm=1e-3)
+        (stp.run_view_grouped if grouped else stp.run_view)(cams[0], target)
+        stp.check()
+        assert model.step == 1
+        out.append((model.m.cpu().numpy()[:11, :sc.n], cb.m.cpu().numpy(), stp.last_grad_norm()))
+    (m0, t0, n0), (m1, t1, n1) = out
+    assert rel_l2(m1, m0) <= 2 * GRAD_TOL and rel_l2(t1, t0) <= 2 * GRAD_TOL
+    assert abs(n1 - n0) <= 2 * GRAD_TOL * n0
+
+
+def test_codebook_training_loop_runs():
+    """Several views through the prefetcher, with more items than one launch of
+    the table's gradient takes; fixed blocks; a view without candidates."""
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper, TargetPrefetcher
+    sc, cams = scene(n=6000, seed=2)
+    rng = np.random.default_rng(1)
+    table = (rng.normal(size=(1500, sc.P - 11)) * 0.2).astype(np.float32)
+    cb = ColorCodebook(table, rng.integers(0, 1500, sc.n))
+    model = GaussianModel(sc.params, sc.n, sc.sh_degree)
+    stp = Stepper(model, codebook=cb, max_grad_norm=0.5, leaf_streams=2)
+    targets = [torch.as_tensor(synth.random_image(160, 120, k) * 0.5).pin_memory() for k in range(3)]
+    feeder = TargetPrefetcher(targets, stepper=stp)
+    for v, target in feeder.iterate([0, 1, 2, 0]):
+        stp.run_view(cams[0], target)
+        stp.check()
+        assert math.isfinite(stp.last_loss()) and stp.last_grad_norm() > 0
+    stp.run_view_blocks(cams[0], targets[0].cuda(), blocks=(2, 2))
+    stp.check()
+    away = synth.Camera(cams[0].R, cams[0].t + np.float32([0, 0, -1e4]), cams[0].fx, cams[0].fy,
+                        cams[0].cx, cams[0].cy, cams[0].width, cams[0].height)
+    before = cb.table.clone()
+    stats = stp.run_view(away, targets[0].cuda())
+    stp.check()
+    assert stats.n_cand == 0 and stp.last_grad_norm() == 0.0
+    assert torch.isfinite(cb.table).all() and not torch.equal(cb.table, before)  # the moments go on
+    assert torch.equal(model.params[11:, :sc.n].t(), cb.table[cb.codes.long()])
+    img = stp.render(cams[0])
+    assert torch.isfinite(img).all()
+
+
+def test_codebook_refusals():
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams = scene(n=30)
+    model = GaussianModel(sc.params, sc.n, sc.sh_degree)
+    table = np.zeros((4, sc.P - 11), np.float32)
+    for cb in (ColorCodebook(table[:, :-1], np.zeros(sc.n, np.int32)),
+               ColorCodebook(table, np.zeros(sc.n - 1, np.int32))):
+        with pytest.raises(ValueError):
+            Stepper(model, codebook=cb)
+    with pytest.raises(ValueError):
+        Stepper(model).last_grad_norm()

@@ -158,3 +158,25 @@ def test_matrix_descriptors(b):
     t = b.tensor_list([f(59, 70)[:, :64], f(4, 5), f(6, 3)[:, :1], f(0), f(2, 3, 4)])
     got = [(x.rows, x.cols, x.row_stride) for x in t.array]
     assert got == [(59, 64, 70), (1, 20, 20), (6, 1, 3), (1, 0, 0), (1, 24, 24)]
+
+
+def test_codebook_and_stepper_check_their_options():
+    """On the host, without device work."""
+    import numpy as np
+    from gaussian_splatting_differentiable_dgs_b200 import synth
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    table = np.zeros((4, 48), np.float32)
+    for bad in (np.zeros(3), np.zeros((3, 1), np.int32), np.array([0, 4])):
+        with pytest.raises(ValueError):
+            ColorCodebook(table, bad, device="cpu")
+    with pytest.raises(ValueError):
+        ColorCodebook(table[0], np.zeros(3, np.int32), device="cpu")
+    cb = ColorCodebook(table, np.array([0, 3, -1]), device="cpu")
+    assert cb.codes.dtype == torch.int32 and (cb.rows, cb.cols) == (4, 48)
+    sc, _ = synth.tiny_scene(n=4)
+    model = GaussianModel(np.asarray(sc.params), sc.n, sc.sh_degree, device="cpu")
+    for kw in ({"max_grad_norm": -1.0}, {"max_grad_norm": float("nan")},
+               {"max_grad_norm": float("inf")}, {"codebook": cb}):
+        with pytest.raises(ValueError):
+            Stepper(model, device="cpu", **kw)
