@@ -276,8 +276,12 @@ __device__ __forceinline__ void adam_vals(float& p, float& m, float& v, float g,
 // gs_grad_norm as it is read, so clipping costs no pass of its own.  A thread
 // owns V neighbouring Gaussians (one 16-byte vector of p, m and v each where
 // the planes allow it) in kAdamPlanes planes; all loads of its planes are
-// issued before the first is used.
-constexpr int kAdamPlanes = 4;
+// issued before the first is used.  Nothing is read or written twice, so the
+// accesses are marked as streaming (evict first).  Bound by HBM: norm and
+// update of 3M Gaussians with 59 planes and 1.25M candidates move 4.85 GB in
+// 812 us; 846 without the marks, 927 with four planes and neither, 890 with
+// one plane.
+constexpr int kAdamPlanes = 2;
 
 template <int V>
 __global__ void __launch_bounds__(kThreads)
@@ -304,9 +308,9 @@ k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__
     const int64_t at = (int64_t)(plane0 + q) * n_pad + i;
     const float* gp = g + (int64_t)(plane0 + q) * g_stride;
     if (V == 4 && cnt == 4) {
-      *reinterpret_cast<float4*>(pp[q]) = *reinterpret_cast<const float4*>(P + at);
-      *reinterpret_cast<float4*>(mm[q]) = *reinterpret_cast<const float4*>(m + at);
-      *reinterpret_cast<float4*>(vv[q]) = *reinterpret_cast<const float4*>(v + at);
+      *reinterpret_cast<float4*>(pp[q]) = __ldcs(reinterpret_cast<const float4*>(P + at));
+      *reinterpret_cast<float4*>(mm[q]) = __ldcs(reinterpret_cast<const float4*>(m + at));
+      *reinterpret_cast<float4*>(vv[q]) = __ldcs(reinterpret_cast<const float4*>(v + at));
     } else {
 #pragma unroll
       for (int k = 0; k < V; ++k)
@@ -334,9 +338,9 @@ k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__
       adam_vals(pp[q][k], mm[q][k], vv[q][k], x, a);
     }
     if (V == 4 && cnt == 4) {
-      *reinterpret_cast<float4*>(P + at) = *reinterpret_cast<const float4*>(pp[q]);
-      *reinterpret_cast<float4*>(m + at) = *reinterpret_cast<const float4*>(mm[q]);
-      *reinterpret_cast<float4*>(v + at) = *reinterpret_cast<const float4*>(vv[q]);
+      __stcs(reinterpret_cast<float4*>(P + at), *reinterpret_cast<const float4*>(pp[q]));
+      __stcs(reinterpret_cast<float4*>(m + at), *reinterpret_cast<const float4*>(mm[q]));
+      __stcs(reinterpret_cast<float4*>(v + at), *reinterpret_cast<const float4*>(vv[q]));
     } else {
 #pragma unroll
       for (int k = 0; k < V; ++k)

@@ -15,13 +15,13 @@ namespace gs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnitBytes = 16384;  // bytes of a row that a block takes at a time
+constexpr int kUnitBytes = 32768;  // bytes of a row that a block takes at a time
 constexpr int kFlatUnit = 4096;    // elements, where rows are too short for that
 constexpr int kShortRow = 1024;    // columns below which rows are short
 constexpr int kMaxTensors = 256;   // tensors per launch, passed by value
-constexpr int kFewTensors = 16;    // ... in a table that is quicker to pass
-constexpr int kNormBlocks = 148 * 8;
-constexpr int kClipBlocks = 148 * 8;
+constexpr int kFewTensors = 16, kSomeTensors = 64;  // ... in tables that are quicker to pass
+constexpr int kNormBlocks = 148 * 32;
+constexpr int kClipBlocks = 148 * 64;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -239,7 +239,7 @@ k_clip(const __grid_constant__ Table<N> tab, const float* __restrict__ clip) {
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       const int i = threadIdx.x + k * kThreads;
-      if (i < x.nv) buf[k].raw = *(reinterpret_cast<const uint4*>(x.src + x.head) + i);
+      if (i < x.nv) buf[k].raw = __ldcs(reinterpret_cast<const uint4*>(x.src + x.head) + i);
     }
     x.ends([&](int i) { put(x.dst + i, c * to_f(x.src[i])); });
 #pragma unroll
@@ -250,7 +250,7 @@ k_clip(const __grid_constant__ Table<N> tab, const float* __restrict__ clip) {
 #pragma unroll
       for (int j = 0; j < V; ++j) put(&w.x[j], c * to_f(buf[k].x[j]));
       if (aligned_dst) {
-        *(reinterpret_cast<uint4*>(x.dst + x.head) + i) = w.raw;
+        __stcs(reinterpret_cast<uint4*>(x.dst + x.head) + i, w.raw);
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) x.dst[x.head + i * V + j] = w.x[j];
@@ -392,8 +392,10 @@ extern "C" gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, doubl
   if (!aligned(ws, 256)) return GS_ERR_ARG;
   const CoefArgs a{max_norm, eps, clip, dev_status};
   double* part = static_cast<double*>(ws);
-  return count <= kFewTensors ? norm_impl<kFewTensors>(tensors, count, part, a, to_stream(stream))
-                              : norm_impl<kMaxTensors>(tensors, count, part, a, to_stream(stream));
+  cudaStream_t s = to_stream(stream);
+  if (count <= kFewTensors) return norm_impl<kFewTensors>(tensors, count, part, a, s);
+  if (count <= kSomeTensors) return norm_impl<kSomeTensors>(tensors, count, part, a, s);
+  return norm_impl<kMaxTensors>(tensors, count, part, a, s);
 }
 
 extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, int32_t count,
@@ -409,6 +411,8 @@ extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, in
     if (a == b && x.row_stride == y.row_stride) continue;
     if (extent(x) && a < b + extent(y) && b < a + extent(x)) return GS_ERR_ARG;
   }
-  return count <= kFewTensors ? clip_impl<kFewTensors>(src, dst, count, clip, to_stream(stream))
-                              : clip_impl<kMaxTensors>(src, dst, count, clip, to_stream(stream));
+  cudaStream_t s = to_stream(stream);
+  if (count <= kFewTensors) return clip_impl<kFewTensors>(src, dst, count, clip, s);
+  if (count <= kSomeTensors) return clip_impl<kSomeTensors>(src, dst, count, clip, s);
+  return clip_impl<kMaxTensors>(src, dst, count, clip, s);
 }

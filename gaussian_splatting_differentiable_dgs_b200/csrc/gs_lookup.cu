@@ -289,7 +289,8 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
             *reinterpret_cast<const uint4*>(s_rows + j * kStagePitch + 4 * q);
         const bool has = s_id[j] >= 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i * cs + j] = from_f<TO>(has ? scale * element<TT>(x, i) : 0.f);
+        for (int i = 0; i < V; ++i)
+          __stcs(o + i * cs + j, from_f<TO>(has ? scale * element<TT>(x, i) : 0.f));
       }
     }
     __syncthreads();
