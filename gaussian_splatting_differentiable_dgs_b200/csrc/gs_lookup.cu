@@ -227,13 +227,13 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
 
 // out in planes, rows of more than 32 bytes on 16-byte boundaries: a block
 // fetches the rows of kTurnItems items (192 bytes of them at a time) into
-// shared memory by asynchronous copies with lanes along the rows, so that a
-// line is one request (a lane that reads its own row makes a request for
-// every 32 bytes: 309 us at 6M x 48), and a warp writes four (eight) planes'
+// shared memory by one bulk copy each, and a warp writes four (eight) planes'
 // pieces of 128 items from there, 16 bytes of a row at a time.  The row pitch
 // of 4 words more than a multiple of 16 keeps those reads free of bank
-// conflicts.  Pieces of a plane must be long: single warps that wrote 32
-// items of all planes in turn took 286 us.
+// conflicts.  Bound by the SMs' requests to L2: 6M x 48 fp32 take 233 us (5.1
+// TB/s written and read); 271 with 16-byte asynchronous copies, 309 with a
+// lane reading its own row (a request for every 32 bytes), 310 with the
+// planes' pieces turned once more and stored in bulk.
 constexpr int kTurnItems = 256;
 constexpr int kStageVecs = 12, kStagePitch = 4 * kStageVecs + 4;  // words
 constexpr size_t kStageSmem = sizeof(uint32_t) * kTurnItems * kStagePitch;
@@ -242,6 +242,17 @@ __device__ __forceinline__ void copy_16_async(void* smem, const void* p, bool ha
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(p),
                "r"(has ? 16 : 0)
                : "memory");
+}
+
+// Waits (bounded) for the bulk copies of the barrier's phase; on expiry sets
+// the flag, waits once more so that none lands in memory given up, and
+// returns false.
+__device__ __forceinline__ bool copies_landed(unsigned long long* bar, unsigned phase,
+                                              int32_t* dev_status) {
+  if (mbar_wait(bar, phase)) return true;
+  dev_flag(dev_status, GS_DEV_TIMEOUT);
+  mbar_wait(bar, phase);
+  return false;
 }
 
 template <class TT, class TO>
@@ -254,6 +265,12 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   static_assert(kThreads == kTurnItems, "a thread for each item's id");
   extern __shared__ __align__(16) uint32_t s_rows[];
   __shared__ int32_t s_id[kTurnItems];
+  __shared__ unsigned long long s_bar;
+  unsigned phase = 0;
+  if (threadIdx.x == 0) {
+    mbar_init(&s_bar, 1);
+    fence_mbar_init();
+  }
   wait_for_prior_grids();
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
@@ -262,20 +279,19 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   __syncthreads();
   for (int c0 = 0; c0 < cols; c0 += kStageVecs * V) {
     const int nv = min(kStageVecs, (cols - c0) / V);
-    int r = t / nv, v = t - r * nv;
-    const int dr = kThreads / nv, dv = kThreads - dr * nv;
-    for (int e = t; e < items * nv; e += kThreads) {
-      const int32_t id = s_id[r];
-      copy_16_async(s_rows + r * kStagePitch + 4 * v,
-                    table + (int64_t)(id < 0 ? 0 : id) * ld + c0 + v * V, id >= 0);
-      r += dr;
-      v += dv;
-      if (v >= nv) {
-        v -= nv;
-        ++r;
-      }
+    // a row per thread: one bulk copy, or zeros
+    const int32_t id = s_id[t];
+    const int rows_in = __syncthreads_count(id >= 0);
+    if (t == 0) mbar_arrive_expect_tx(&s_bar, (unsigned)(rows_in * nv * 16));
+    __syncthreads();
+    uint32_t* d = s_rows + t * kStagePitch;
+    if (id >= 0) {
+      bulk_load(d, table + (int64_t)id * ld + c0, nv * 16, &s_bar);
+    } else {
+      for (int v = 0; v < nv; ++v) *reinterpret_cast<uint4*>(d + 4 * v) = make_uint4(0, 0, 0, 0);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!copies_landed(&s_bar, phase, dev_status)) return;
+    phase ^= 1;
     __syncthreads();
     for (int u = w; u < nv * (kTurnItems / PIECE); u += W) {
       const int q = u / (kTurnItems / PIECE);
@@ -305,6 +321,12 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
 // bit more than the rows do.  Against the library's general 32-bit sort (8
 // bits per pass, an even number of passes, a histogram before them, tiles of
 // 4096) 2.5M items over 2^16 rows take half the time.
+// For few items the kernels' launches are what costs: up to kFewTiles tiles
+// the scatter sums the tiles' counts itself and counts the next pass's digits
+// as it writes (integer atomics: the counts do not depend on their order), so
+// that a pass is one launch after the first.  100K items x 16 take 33 us so,
+// 40 without; 300K take 45 and 42.
+constexpr int kFewTiles = 64;
 constexpr int kSortItems = 8, kSortTile = kThreads * kSortItems, kMaxDigit = 10;
 
 struct Ids {
@@ -313,13 +335,14 @@ struct Ids {
   int64_t n_ids, rows;
 };
 
-// counts[digit][tile]; the first pass also writes the pairs and clears `zeros`
-// floats of dtable
+// counts[digit][tile] (few tiles: counts[tile][digit]); the first pass also
+// writes the pairs and clears the `later` passes' counts, which follow, and
+// `zeros` floats of dtable
 template <bool FIRST>
 __global__ void __launch_bounds__(kThreads)
 k_sort_count(const __grid_constant__ Ids src, uint2* __restrict__ pairs, int64_t n, int shift,
-             int bits, uint32_t* __restrict__ counts, float* __restrict__ dtable, int64_t zeros,
-             int32_t* dev_status) {
+             int bits, uint32_t* __restrict__ counts, bool few, int later, float* __restrict__ dtable,
+             int64_t zeros, int32_t* dev_status) {
   __shared__ uint32_t s_hist[1 << kMaxDigit];
   wait_for_prior_grids();
   const int t = threadIdx.x, bins = 1 << bits;
@@ -354,8 +377,10 @@ k_sort_count(const __grid_constant__ Ids src, uint2* __restrict__ pairs, int64_t
       if (j < n) pairs[j] = make_uint2(key[i], id[i] >= 0 ? (uint32_t)j : 0xffffffffu);
     }
     if (bad) dev_flag(dev_status, GS_DEV_BOUNDS);
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < zeros; i += (int64_t)gridDim.x * kThreads)
-      dtable[i] = 0.f;
+    const int64_t quads = zeros / 4, at0 = (int64_t)blockIdx.x * kThreads + t;
+    for (int64_t i = at0; i < quads; i += (int64_t)gridDim.x * kThreads)
+      reinterpret_cast<uint4*>(dtable)[i] = make_uint4(0, 0, 0, 0);
+    if (at0 < zeros % 4) dtable[4 * quads + at0] = 0.f;
   } else {
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
@@ -367,7 +392,13 @@ k_sort_count(const __grid_constant__ Ids src, uint2* __restrict__ pairs, int64_t
   for (int i = 0; i < kSortItems; ++i)
     if (j0 + i * kThreads < n) atomicAdd(&s_hist[(key[i] >> shift) & (bins - 1)], 1u);
   __syncthreads();
-  for (int d = t; d < bins; d += kThreads) counts[(int64_t)d * gridDim.x + blockIdx.x] = s_hist[d];
+  for (int d = t; d < bins; d += kThreads)
+    counts[few ? (int64_t)blockIdx.x * bins + d : (int64_t)d * gridDim.x + blockIdx.x] = s_hist[d];
+  if (FIRST && later > 0) {
+    const int64_t size = (int64_t)gridDim.x * bins;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < size * later; i += (int64_t)gridDim.x * kThreads)
+      counts[size + i] = 0;
+  }
 }
 
 // counts of digit blockIdx.x -> exclusive sums over the tiles; total[digit]
@@ -401,10 +432,12 @@ size_t scatter_smem(int bits) {
   return sizeof(uint2) * kSortTile + ((size_t)1 << bits) * (2 * sizeof(uint32_t) + 2 * (kThreads / 32));
 }
 
+// FEW: counts[tile][digit] of this pass; next: those of the next pass (or null)
+template <bool FEW>
 __global__ void __launch_bounds__(kThreads, 5)
 k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
                const uint32_t* __restrict__ counts, const uint32_t* __restrict__ total,
-               uint2* __restrict__ out) {
+               uint32_t* __restrict__ next, uint2* __restrict__ out) {
   constexpr int kWarps = kThreads / 32, kPer = (1 << kMaxDigit) / kThreads;
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ unsigned long long s_scan[kWarps + 1];
@@ -431,8 +464,20 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
   for (int i = 0; i < kPer; ++i) {
     const int d = t * per + i;
     const bool in = i < per && d < bins;
-    tot[i] = in ? total[d] : 0;
-    cnt[i] = in ? counts[(int64_t)d * gridDim.x + blockIdx.x] : 0;
+    if (!FEW) {
+      tot[i] = in ? total[d] : 0;
+      cnt[i] = in ? counts[(int64_t)d * gridDim.x + blockIdx.x] : 0;
+    } else {
+      tot[i] = cnt[i] = 0;
+      if (in) {
+#pragma unroll 16
+        for (int k = 0; k < (int)gridDim.x; ++k) {
+          const uint32_t c = counts[k * bins + d];
+          tot[i] += c;
+          if (k < (int)blockIdx.x) cnt[i] += c;
+        }
+      }
+    }
   }
   for (int i = t; i < bins * kWarps / 2; i += kThreads) reinterpret_cast<uint32_t*>(s_hist)[i] = 0;
   __syncthreads();
@@ -498,7 +543,10 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
     const int i = t + k * kThreads;
     if (i < items) {
       const uint2 x = s_pair[i];
-      out[s_base[(x.x >> shift) & (bins - 1)] + i] = x;
+      const uint32_t at = s_base[(x.x >> shift) & (bins - 1)] + i;
+      out[at] = x;
+      if (FEW && next)
+        atomicAdd(&next[at / kSortTile * bins + ((x.x >> (shift + bits)) & (bins - 1))], 1u);
     }
   }
 }
@@ -1115,7 +1163,8 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   const Passes ps(rows);
   w.pairs[0] = cv.take<uint2>(n);
   w.pairs[1] = cv.take<uint2>(n);
-  w.counts = cv.take<uint32_t>(((size_t)1 << ps.bits) * ((n + kSortTile - 1) / kSortTile));
+  const int64_t tiles = (n + kSortTile - 1) / kSortTile;
+  w.counts = cv.take<uint32_t>(((size_t)1 << ps.bits) * tiles * (tiles <= kFewTiles ? ps.count : 1));
   w.total = cv.take<uint32_t>((size_t)1 << ps.bits);
   // partials: the most that any type and alignment leaves
   int64_t m = n;
@@ -1165,18 +1214,29 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
   const Passes ps(rows);
   const Ids src{ids, index, n_ids, rows};
   const unsigned tiles = (unsigned)((n + kSortTile - 1) / kSortTile);
+  const bool few = tiles <= kFewTiles;
+  uint32_t* counts = w.counts;
   for (int p = 0; p < ps.count; ++p) {
     uint2* from = w.pairs[(ps.count - p) & 1];
     uint2* to = w.pairs[(ps.count - 1 - p) & 1];
     const int shift = p * ps.bits;
-    GS_TRY(launch_dependent(p == 0 ? k_sort_count<true> : k_sort_count<false>, tiles, kThreads, 0, s,
-                            src, from, n, shift, ps.bits, w.counts, dtable, zeros, dev_status));
+    if (p == 0 || !few) {
+      GS_TRY(launch_dependent(p == 0 ? k_sort_count<true> : k_sort_count<false>, tiles, kThreads, 0, s,
+                              src, from, n, shift, ps.bits, counts, few, few ? ps.count - 1 : 0,
+                              dtable, zeros,
+                              dev_status));
+      GS_LAUNCH_CHECK();
+    }
+    uint32_t* next = few && p + 1 < ps.count ? counts + ((size_t)tiles << ps.bits) : nullptr;
+    if (!few) {
+      GS_TRY(launch_dependent(k_sort_scan, 1u << ps.bits, kThreads, 0, s, counts, tiles, w.total));
+      GS_LAUNCH_CHECK();
+    }
+    GS_TRY(launch_dependent(few ? k_sort_scatter<true> : k_sort_scatter<false>, tiles, kThreads,
+                            scatter_smem(ps.bits), s, from, n, shift, ps.bits, counts, w.total, next,
+                            to));
     GS_LAUNCH_CHECK();
-    GS_TRY(launch_dependent(k_sort_scan, 1u << ps.bits, kThreads, 0, s, w.counts, tiles, w.total));
-    GS_LAUNCH_CHECK();
-    GS_TRY(launch_dependent(k_sort_scatter, tiles, kThreads, scatter_smem(ps.bits), s, from, n, shift,
-                            ps.bits, w.counts, w.total, to));
-    GS_LAUNCH_CHECK();
+    if (next) counts = next;
   }
   return GS_OK;
 }
@@ -1438,10 +1498,10 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
   const bool plan = !(flags & GS_LOOKUP_PLANNED) && sorted;
   float* dt = static_cast<float*>(dtable->data);
   // rows that no item uses: cleared by the sort's first kernel where the table
-  // is contiguous and no block of it gets more than 32 KB to clear
+  // is contiguous and no block of it gets more than 256 KB to clear
   const int64_t elements = rows * dtable->cols, tiles = (n + kSortTile - 1) / kSortTile;
   const bool fused = plan && !accumulate && dtable->row_stride == dtable->cols &&
-                     elements <= tiles * 8192;
+                     aligned(dt, 16) && elements <= tiles * 65536;
   if (!accumulate && !fused && (n == 0 || sorted))
     GS_TRY(cudaMemset2DAsync(dt, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
   if (n == 0) return GS_OK;
