@@ -1118,7 +1118,7 @@ k_join_tables(const float* __restrict__ partial, int64_t splits, int cols, int r
   float sum = 0.f;
   if (e < total) {
     const float* p = partial + e;
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t i = a; i < b; ++i) sum += p[i * total];
   }
   s_sum[w][lane] = sum;
