@@ -569,6 +569,8 @@ def matrix(t) -> gs_matrix:
         raise ValueError("a matrix is a 2-D float32, float16 or bfloat16 tensor, not "
                          f"{t.dim()}-D {t.dtype}")
     rows, cols = shape
+    if cols > 0x7fffffff:
+        raise ValueError(f"a matrix has at most 2^31 - 1 columns, not {cols}")
     rs, cs = t.stride()
     # the stride of an axis of one element is arbitrary
     if cols == 1 and not (rs == 1 and cs >= rows):

@@ -312,7 +312,9 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // leave no error for the next call
+  return e;
 }
 
 // 32-bit key sort with values 0..count-1, the count read on the device (at

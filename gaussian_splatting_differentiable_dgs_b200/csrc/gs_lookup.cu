@@ -653,8 +653,8 @@ template <class T, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
 k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, int64_t n,
            const __grid_constant__ RunShape sh, const T* __restrict__ g, int64_t rs, int cols,
-           float scale, float* __restrict__ dtable, int64_t ld, bool accumulate,
-           uint32_t* __restrict__ pkey, float* __restrict__ psum, int ldp) {
+           float scale, float* __restrict__ dtable, int64_t ld, uint32_t rows, bool accumulate,
+           uint32_t* __restrict__ pkey, float* __restrict__ psum, int ldp, int32_t* dev_status) {
   extern __shared__ __align__(16) unsigned char s_row[];  // [entries][pitch]
   __shared__ bool s_start[kMaxTeams], s_whole[kMaxTeams];
   const int pitch = sh.pitch, len = sh.len;
@@ -669,14 +669,20 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   const int width = min(sh.width, (cols + V - 1) / V - v0);
   for (int i = t; i < m; i += kThreads) {
     if (FIRST) {
+      // a kept order that is none (memory that no plan wrote) stays in bounds
       const uint2 p = pairs[A + i];
-      s_key[i] = p.x;
-      s_item[i] = (int32_t)p.y;
+      const bool good = p.x < rows && ((int32_t)p.y < 0 || p.y < n);
+      if (!good) dev_flag(dev_status, GS_DEV_BOUNDS);
+      s_key[i] = good ? p.x : kNoRow;
+      s_item[i] = good ? (int32_t)p.y : -1;
     } else {
       s_key[i] = keys[A + i];
     }
   }
-  const auto key_at = [&](int64_t r) { return FIRST ? pairs[r].x : keys[r]; };
+  const auto key_at = [&](int64_t r) {
+    const uint32_t k = FIRST ? pairs[r].x : keys[r];
+    return FIRST && k >= rows ? kNoRow : k;
+  };
   const uint32_t before = A > 0 ? key_at(A - 1) : kNoRow, after = A + m < n ? key_at(A + m) : kNoRow;
   __syncthreads();
   {
@@ -1243,31 +1249,33 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
 
 template <class T, int V, bool FIRST>
 gs_status launch_sums(const uint2* pairs, const uint32_t* keys, int64_t n, const RunShape& sh,
-                      const T* g, int64_t rs, int cols, float scale, float* dt, int64_t ld,
-                      bool accumulate, uint32_t* pkey, float* psum, int ldp, cudaStream_t s) {
+                      const T* g, int64_t rs, int cols, float scale, const gs_matrix* dtable,
+                      bool accumulate, uint32_t* pkey, float* psum, int ldp, int32_t* dev_status,
+                      cudaStream_t s) {
   if (sh.blocks * sh.col_tiles > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;
   static std::atomic<unsigned long long> once{0};
   GS_TRY(smem_attrs_once((const void*)k_run_sums<T, V, FIRST>,
                          kRunRowBytes + 2 * kThreads * V * 4 + kRunEntries * 8, &once));
   GS_TRY(launch_dependent(k_run_sums<T, V, FIRST>, (unsigned)(sh.blocks * sh.col_tiles), kThreads,
-                          sh.smem, s, pairs, keys, n, sh, g, rs, cols, scale, dt, ld, accumulate,
-                          pkey, psum, ldp));
+                          sh.smem, s, pairs, keys, n, sh, g, rs, cols, scale,
+                          static_cast<float*>(dtable->data), dtable->row_stride,
+                          (uint32_t)dtable->rows, accumulate, pkey, psum, ldp, dev_status));
   GS_LAUNCH_CHECK();
   return GS_OK;
 }
 
 template <class T, int V>
-gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, float* dt, int64_t ld,
-                   bool accumulate, const LookupWs& w, cudaStream_t s) {
+gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, const gs_matrix* dtable,
+                   bool accumulate, const LookupWs& w, int32_t* dev_status, cudaStream_t s) {
   RunShape sh(n, cols, V, sizeof(T), true);
-  gs_status st = launch_sums<T, V, true>(w.pairs[0], nullptr, n, sh, g, rs, cols, scale, dt, ld,
-                                         accumulate, w.pkey[0], w.psum[0], w.ldp, s);
+  gs_status st = launch_sums<T, V, true>(w.pairs[0], nullptr, n, sh, g, rs, cols, scale, dtable,
+                                         accumulate, w.pkey[0], w.psum[0], w.ldp, dev_status, s);
   for (int from = 0; st == GS_OK && sh.blocks > 1; from ^= 1) {
     const int64_t m = 2 * sh.blocks;
     sh = RunShape(m, cols, 4, 4, false);
     st = launch_sums<float, 4, false>(nullptr, w.pkey[from], m, sh, w.psum[from], w.ldp, cols, scale,
-                                      dt, ld, accumulate, w.pkey[from ^ 1], w.psum[from ^ 1], w.ldp,
-                                      s);
+                                      dtable, accumulate, w.pkey[from ^ 1], w.psum[from ^ 1], w.ldp,
+                                      dev_status, s);
   }
   return st;
 }
@@ -1456,8 +1464,6 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
   if (ps.use)
     return private_grad<T>(g, Ids{ids, index, n_ids, dtable->rows}, scale, dtable, accumulate, ps,
                            w.partial, dev_status, s);
-  float* dt = static_cast<float*>(dtable->data);
-  const int64_t ld = dtable->row_stride;
   if (planes) {
     const int vecs = (cols + V - 1) / V;
     static std::atomic<unsigned long long> once{0};
@@ -1465,11 +1471,13 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
     GS_TRY(launch_dependent(k_planes_to_rows<T>, (unsigned)((n + kTurnItems - 1) / kTurnItems),
                             kThreads, Turn<T>::kSmem, s, data, g->col_stride, cols, n, w.rows, vecs));
     GS_LAUNCH_CHECK();
-    return run_sums<T, V>(reinterpret_cast<const T*>(w.rows), (int64_t)vecs * V, n, cols, scale, dt,
-                          ld, accumulate, w, s);
+    return run_sums<T, V>(reinterpret_cast<const T*>(w.rows), (int64_t)vecs * V, n, cols, scale,
+                          dtable, accumulate, w, dev_status, s);
   }
-  return vec ? run_sums<T, V>(data, g->row_stride, n, cols, scale, dt, ld, accumulate, w, s)
-             : run_sums<T, 1>(data, g->row_stride, n, cols, scale, dt, ld, accumulate, w, s);
+  return vec ? run_sums<T, V>(data, g->row_stride, n, cols, scale, dtable, accumulate, w,
+                              dev_status, s)
+             : run_sums<T, 1>(data, g->row_stride, n, cols, scale, dtable, accumulate, w,
+                              dev_status, s);
 }
 
 }  // namespace

@@ -350,3 +350,51 @@ def test_lookup_capacity(b):
     with pytest.raises(b.GsError) as e:
         b.gs_lookup_bwd(g, ids, torch.empty(10, 8, device="cuda"), ws)
     assert e.value.status == b.GS_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("n", [40, 3001])
+@pytest.mark.parametrize("cols", [1500, 2051])
+@pytest.mark.parametrize("kind", ["rows", "planes"])
+def test_wide_rows(b, n, cols, kind):
+    """More columns than a block takes at a time, with few and many table rows."""
+    for rows in (10, 1500):
+        ids = make_ids(n, rows, n + rows)
+        table = torch.randn(rows, cols, generator=gen(81), device="cuda")
+        out = layout(torch.zeros(n, cols, device="cuda"), kind)
+        b.gs_lookup(table, ids, out)
+        assert torch.equal(out, torch.where((ids >= 0)[:, None], table[ids.clamp(min=0).long()], 0.0))
+        for dtype in (torch.float32, torch.bfloat16):
+            g = torch.randn(n, cols, generator=gen(82), device="cuda").to(dtype)
+            check_grad(run_grad(b, layout(g, kind), ids, rows), exact_grad(g, ids, rows, 1.0))
+
+
+def test_two_calls_at_once(b):
+    """Gradients on two streams with workspaces of their own."""
+    n, rows, cols = 60_000, 5000, 27
+    data = [(torch.randn(n, cols, generator=gen(90 + k), device="cuda"), make_ids(n, rows, 92 + k))
+            for k in range(2)]
+    out = [torch.empty(rows, cols, device="cuda") for _ in range(2)]
+    ws = [torch.empty(b.gs_lookup_bwd_workspace_size(g, rows), dtype=torch.uint8, device="cuda")
+          for g, _ in data]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, (g, ids) in enumerate(data):
+            b.gs_lookup_bwd(g, ids, out[k], ws[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k, (g, ids) in enumerate(data):
+        assert torch.equal(out[k], run_grad(b, g, ids, rows))
+
+
+def test_kept_order_with_planes_of_a_small_table(b):
+    """A gradient in planes that needs no order leaves a kept one as it is."""
+    n, rows, cols = 9000, 200, 12
+    ids = make_ids(n, rows, 95)
+    g = torch.randn(n, cols, generator=gen(96), device="cuda")
+    planar = g.t().contiguous().t()
+    ws = torch.empty(b.gs_lookup_bwd_workspace_size(planar, rows), dtype=torch.uint8, device="cuda")
+    b.gs_lookup_plan(ids, n, rows, cols, ws)
+    for _ in range(2):
+        for x in (planar, g):
+            got = b.gs_lookup_bwd(x, ids, torch.empty(rows, cols, device="cuda"), ws, planned=True)
+            check_grad(got, exact_grad(g, ids, rows, 1.0))
