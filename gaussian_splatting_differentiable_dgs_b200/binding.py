@@ -519,16 +519,16 @@ GS_LOOKUP_PLANNED = 2
 
 
 _codes = {}       # torch dtype -> GS_* element type, filled on first use
-_int32 = None
+_int32 = _float32 = None
 _get_device = _raw_stream = None
 
 
 def _torch_names():
-    global _int32, _get_device, _raw_stream
+    global _int32, _float32, _get_device, _raw_stream
     import torch
     _codes.update({torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16})
-    _int32 = torch.int32
-    _get_device = torch.cuda.current_device
+    _int32, _float32 = torch.int32, torch.float32
+    _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -536,12 +536,11 @@ def _torch_names():
 def _call(name, dev, stream, fn, *args):
     """fn(*args, stream) with `dev` current: kernels, their attributes and the
     default stream belong to a device."""
-    if dev == _get_device():
-        st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    else:
+    if dev != _get_device():
         import torch
         with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+            return _call(name, dev, stream, fn, *args)
+    st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     return st if st >= 0 else _ok(name, st)
 
 
@@ -550,10 +549,10 @@ def _device(name, first, *rest):
     if _int32 is None:
         _torch_names()
     dev = first.get_device()
-    ok = dev >= 0
     for t in rest:
-        ok = ok and (t is None or t.get_device() == dev)
-    if not ok:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
         raise ValueError(f"{name}: tensors must be on one CUDA device")
     return dev
 
@@ -564,13 +563,14 @@ def matrix(t) -> gs_matrix:
     if _int32 is None:
         _torch_names()
     code = _codes.get(t.dtype)
-    shape = t.shape
-    if code is None or len(shape) != 2:
+    if code is None or t.dim() != 2:
         raise ValueError("a matrix is a 2-D float32, float16 or bfloat16 tensor, not "
                          f"{t.dim()}-D {t.dtype}")
-    rows, cols = shape
+    rows, cols = t.shape
     if cols > 0x7fffffff:
         raise ValueError(f"a matrix has at most 2^31 - 1 columns, not {cols}")
+    if t.is_contiguous():
+        return gs_matrix(t.data_ptr(), rows, cols, 1, cols, code)
     rs, cs = t.stride()
     # the stride of an axis of one element is arbitrary
     if cols == 1 and not (rs == 1 and cs >= rows):
@@ -608,8 +608,9 @@ def gs_lookup(table, ids, out, scale=1.0, index=None, dev_status=None, stream=No
     t, o = matrix(table), matrix(out)
     n_ids = _items(ids, index, o.rows)
     dev = _device("gs_lookup", table, ids, out, index, dev_status)
-    _call("gs_lookup", dev, stream, _L.gs_lookup, t, ids.data_ptr(), n_ids, ptr(index), scale, o,
-          ptr(dev_status))
+    _call("gs_lookup", dev, stream, _L.gs_lookup, t, ids.data_ptr(), n_ids,
+          None if index is None else index.data_ptr(), scale, o,
+          None if dev_status is None else dev_status.data_ptr())
     return out
 
 
@@ -684,8 +685,9 @@ def gs_grad_norm_workspace_size(tensors) -> int:
 
 
 def _clip_device(name, clip, ws, dev_status, *lists):
-    import torch
-    if clip.dtype is not torch.float32 or clip.numel() < 2 or not clip.is_contiguous():
+    if _int32 is None:
+        _torch_names()
+    if clip.dtype is not _float32 or clip.numel() < 2 or not clip.is_contiguous():
         raise ValueError("clip must be a contiguous float32 tensor of 2 values")
     dev = _device(name, clip, ws, dev_status)
     for x in lists:
