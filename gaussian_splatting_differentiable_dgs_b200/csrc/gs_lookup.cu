@@ -225,7 +225,7 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
   }
 }
 
-// out in planes, rows of more than 32 bytes on 16-byte boundaries: a block
+// out in planes, rows of more than 64 bytes on 16-byte boundaries: a block
 // fetches the rows of kTurnItems items (192 bytes of them at a time) into
 // shared memory by one bulk copy each, and a warp writes four (eight) planes'
 // pieces of 128 items from there, 16 bytes of a row at a time.  The row pitch
@@ -264,7 +264,7 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   constexpr int V = 16 / sizeof(TT), W = kThreads / 32, PIECE = 128;
   static_assert(kThreads == kTurnItems, "a thread for each item's id");
   extern __shared__ __align__(16) uint32_t s_rows[];
-  __shared__ int32_t s_id[kTurnItems];
+  __shared__ int16_t s_from[kTurnItems];  // the row that holds an item's values; -1: zeros
   __shared__ unsigned long long s_bar;
   unsigned phase = 0;
   if (threadIdx.x == 0) {
@@ -275,21 +275,21 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
   const int items = (int)min((int64_t)kTurnItems, n - j0);
-  s_id[t] = t < items ? id_of(ids, n_ids, index, j0 + t, rows, dev_status) : -1;
+  const int32_t id = t < items ? id_of(ids, n_ids, index, j0 + t, rows, dev_status) : -1;
+  // lanes with the same id share the first one's copy: a row that many items
+  // use would otherwise be fetched from one place of L2 by all SMs at once
+  // (64 columns of a one-row table: 584 us without this)
+  const int leader = __ffs(__match_any_sync(0xffffffffu, id)) - 1;
+  const bool fetch = id >= 0 && leader == lane;
+  s_from[t] = id >= 0 ? (int16_t)(t - lane + leader) : -1;
   __syncthreads();
   for (int c0 = 0; c0 < cols; c0 += kStageVecs * V) {
     const int nv = min(kStageVecs, (cols - c0) / V);
-    // a row per thread: one bulk copy, or zeros
-    const int32_t id = s_id[t];
-    const int rows_in = __syncthreads_count(id >= 0);
-    if (t == 0) mbar_arrive_expect_tx(&s_bar, (unsigned)(rows_in * nv * 16));
+    // a row per thread: one bulk copy
+    const int copies = __syncthreads_count(fetch);
+    if (t == 0) mbar_arrive_expect_tx(&s_bar, (unsigned)(copies * nv * 16));
     __syncthreads();
-    uint32_t* d = s_rows + t * kStagePitch;
-    if (id >= 0) {
-      bulk_load(d, table + (int64_t)id * ld + c0, nv * 16, &s_bar);
-    } else {
-      for (int v = 0; v < nv; ++v) *reinterpret_cast<uint4*>(d + 4 * v) = make_uint4(0, 0, 0, 0);
-    }
+    if (fetch) bulk_load(s_rows + t * kStagePitch, table + (int64_t)id * ld + c0, nv * 16, &s_bar);
     if (!copies_landed(&s_bar, phase, dev_status)) return;
     phase ^= 1;
     __syncthreads();
@@ -300,10 +300,11 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
       for (int k = 0; k < PIECE / 32; ++k) {
         const int j = u % (kTurnItems / PIECE) * PIECE + k * 32 + lane;
         if (j >= items) break;
+        const int from = s_from[j];
+        const bool has = from >= 0;
         uint32_t x[4];
         *reinterpret_cast<uint4*>(x) =
-            *reinterpret_cast<const uint4*>(s_rows + j * kStagePitch + 4 * q);
-        const bool has = s_id[j] >= 0;
+            *reinterpret_cast<const uint4*>(s_rows + (has ? from : j) * kStagePitch + 4 * q);
 #pragma unroll
         for (int i = 0; i < V; ++i)
           __stcs(o + i * cs + j, from_f<TO>(has ? scale * element<TT>(x, i) : 0.f));
@@ -803,29 +804,39 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   }
 }
 
-// Up to kSmallItems items, in one launch: a block owns a range of the table's
-// rows.  It picks the items with ids in its range (in order), sorts them by id
-// in shared memory (the rank of an item is the number of items before it),
-// sums the runs of equal ids with teams of threads, each a stretch of the
-// sorted list, joins the teams' partial runs in order, and clears the rows
-// that nothing used.  Every block reads all ids.
+// Up to kSmallItems items, in one launch: a block owns a range of up to
+// kSmallRows of the table's rows and of the columns.  It picks the items with
+// ids in its range (in order), sorts them by id in shared memory (the rank of
+// an item among its warp's equal ids from ballots over the id's bits, as in
+// the sort above), sums the runs of equal ids with teams of threads, each a
+// stretch of the sorted list, joins the teams' partial runs in order, and
+// clears the rows that nothing used.  Every block reads all ids.
 constexpr int kSmallItems = 2048, kSmallPer = kSmallItems / kThreads;
-constexpr int kSmallTeams = 64;
+constexpr int kSmallTeams = 64, kSmallRows = 1024;
 
 template <class T, int V>
 __global__ void __launch_bounds__(kThreads)
-k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
-             const int32_t* __restrict__ ids, int64_t n_ids, const int32_t* __restrict__ index, int n,
-             float scale, float* __restrict__ dtable, int64_t ld, int64_t rows, int64_t per,
-             bool accumulate, int32_t* dev_status) {
+k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols, int share,
+             unsigned col_tiles, const int32_t* __restrict__ ids, int64_t n_ids,
+             const int32_t* __restrict__ index, int n, float scale, float* __restrict__ dtable,
+             int64_t ld, int64_t rows, int per, bool accumulate, int32_t* dev_status) {
+  constexpr int W = kThreads / 32;
   __shared__ int32_t s_key[kSmallItems];
   __shared__ uint16_t s_item[kSmallItems];
-  __shared__ int s_scan[kThreads / 32 + 1];
+  __shared__ int s_scan[W + 1];
   __shared__ int32_t s_pk[2 * kSmallTeams];
-  __shared__ float s_part[2 * kThreads * V];
+  __shared__ uint32_t s_loc[kSmallRows];
+  // the sort's counts [warp][row], then the teams' partial sums
+  __shared__ __align__(16) unsigned char s_both[2 * kSmallRows * W];
+  static_assert(sizeof(float) * 2 * kThreads * V <= sizeof(s_both), "partial sums fit");
+  uint16_t* s_hist = reinterpret_cast<uint16_t*>(s_both);
+  float* s_part = reinterpret_cast<float*>(s_both);
   wait_for_prior_grids();
-  const int t = threadIdx.x;
-  const int64_t k0 = blockIdx.x * per, k1 = min(k0 + per, rows);
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const int64_t k0 = (int64_t)(blockIdx.x / col_tiles) * per, k1 = min(k0 + per, rows);
+  // this block's vectors of V columns
+  const int nv = (cols + V - 1) / V, first = (int)(blockIdx.x % col_tiles) * share;
+  const int last = min(first + share, nv);
   int32_t key[kSmallPer];
   int mine = 0;
 #pragma unroll
@@ -836,17 +847,19 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
     mine += key[i] >= 0;
   }
   if (!accumulate) {
-    float* d = dtable + k0 * ld;
-    if (ld == cols) {
-      const int64_t total = (k1 - k0) * cols;
+    const int c0 = first * V, width = min(last * V, cols) - c0;
+    float* d = dtable + k0 * ld + c0;
+    if (width == ld) {
+      const int64_t total = (k1 - k0) * ld;
       for (int64_t i = t; i < total; i += kThreads) d[i] = 0.f;
     } else {
-      for (int64_t k = k0; k < k1; ++k, d += ld)
-        for (int c = t; c < cols; c += kThreads) d[c] = 0.f;
+      // 32 columns of a warp's row at a time
+      for (int64_t k = w; k < k1 - k0; k += W)
+        for (int c = lane; c < width; c += 32) d[k * ld + c] = 0.f;
     }
   }
   int m;
-  int at = block_exclusive_scan<int, kThreads / 32>(mine, s_scan, &m);
+  int at = block_exclusive_scan<int, W>(mine, s_scan, &m);
   if (m == 0) return;
 #pragma unroll
   for (int i = 0; i < kSmallPer; ++i)
@@ -854,42 +867,68 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
       s_key[at] = key[i];
       s_item[at++] = (uint16_t)(t * kSmallPer + i);
     }
+  const int digits = (int)(k1 - k0);
+  if (digits > 1)
+    for (int i = t; i < (digits * W + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(s_hist)[i] = 0;
   __syncthreads();  // also: the zeros above are ordered before the sums below
-  if (k1 - k0 > 1) {
+  if (digits > 1) {
+    const int bits = 32 - __clz(digits - 1), rounds = (m + kThreads - 1) / kThreads;
+    uint16_t* hist = s_hist + w * digits;
     int32_t mk[kSmallPer];
-    uint16_t mi[kSmallPer];
-    int rank[kSmallPer];
+    uint16_t mi[kSmallPer], rank[kSmallPer];
 #pragma unroll
-    for (int i = 0; i < kSmallPer; ++i) {
-      const int e = t + i * kThreads;
-      if (e < m) {
-        mk[i] = s_key[e];
-        mi[i] = s_item[e];
-        rank[i] = 0;
-        for (int f = 0; f < m; ++f) {
-          const int32_t kf = s_key[f];
-          rank[i] += kf < mk[i] || (kf == mk[i] && f < e);
-        }
+    for (int i = 0; i < kSmallPer; ++i) {  // a warp's items are neighbours
+      if (i >= rounds) break;
+      const int e = (w * rounds + i) * 32 + lane;
+      const bool in = e < m;
+      mk[i] = in ? s_key[e] : 0;
+      mi[i] = in ? s_item[e] : 0;
+      unsigned same = __ballot_sync(0xffffffffu, in);
+      for (int k = 0; k < bits; ++k) {
+        const bool one = (mk[i] >> k) & 1;
+        const unsigned bal = __ballot_sync(0xffffffffu, one);
+        same &= one ? bal : ~bal;
       }
+      const int before = __popc(same & ((1u << lane) - 1)), had = in ? hist[mk[i]] : 0;
+      rank[i] = (uint16_t)(had + before);
+      __syncwarp();
+      if (in && before == 0) hist[mk[i]] = (uint16_t)(had + __popc(same));
+      __syncwarp();
     }
+    __syncthreads();
+    const int each = (digits + kThreads - 1) / kThreads;
+    int local = 0, all;
+    for (int d = t * each; d < min(digits, (t + 1) * each); ++d) {
+      int run = 0;
+      for (int k = 0; k < W; ++k) {
+        const int c = s_hist[k * digits + d];
+        s_hist[k * digits + d] = (uint16_t)run;
+        run += c;
+      }
+      s_loc[d] = local;
+      local += run;
+    }
+    const int base = block_exclusive_scan<int, W>(local, s_scan, &all);
+    for (int d = t * each; d < min(digits, (t + 1) * each); ++d) s_loc[d] += base;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSmallPer; ++i)
-      if (t + i * kThreads < m) {
-        s_key[rank[i]] = mk[i];
-        s_item[rank[i]] = mi[i];
+      if (i < rounds && (w * rounds + i) * 32 + lane < m) {
+        const int p = s_loc[mk[i]] + hist[mk[i]] + rank[i];
+        s_key[p] = mk[i];
+        s_item[p] = mi[i];
       }
     __syncthreads();
   }
-  const int nv = (cols + V - 1) / V;
-  int teams = nv < kThreads ? kThreads / nv : 1;
+  const int mine_v = last - first;
+  int teams = mine_v < kThreads ? kThreads / mine_v : 1;
   teams = min(teams, min(kSmallTeams, (m + 3) / 4));
   const int len = (m + teams - 1) / teams;
-  const int width = nv < kThreads ? nv : kThreads;  // vectors of a row at a time
+  const int width = min(mine_v, kThreads);  // vectors of a row at a time
   const int team = t / width, tv = t - team * width;
-  for (int v0 = 0; v0 < nv; v0 += width) {
+  for (int v0 = first; v0 < last; v0 += width) {
     const int c = (v0 + tv) * V;
-    const bool on = team < teams && c < cols;
+    const bool on = team < teams && v0 + tv < last;
     const int a = team * len, b = min(a + len, m);
     if (on && tv == 0) s_pk[2 * team] = s_pk[2 * team + 1] = -1;
     if (on && a < b) {
@@ -939,7 +978,7 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols,
     }
     __syncthreads();
     // partial runs, joined in order by the first team
-    if (team == 0 && c < cols) {
+    if (team == 0 && on) {
       float sum[V];
       int k = -1;
       auto done = [&]() {
@@ -1311,7 +1350,7 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
     const int cols = o->cols, words = (cols * (int)sizeof(TT) + 3) / 4;
     const int al = vector_of(t->data, t->row_stride, cols, sizeof(TT), 2 * V);
     const unsigned blocks = blocks_for(o->rows);
-    if (al >= V && words > 8) {
+    if (al >= V && words > 16) {
       static std::atomic<unsigned long long> once{0};
       GS_TRY(smem_attrs_once((const void*)k_lookup_planes_staged<TT, TO>, (int)kStageSmem, &once));
       GS_TRY(launch_dependent(k_lookup_planes_staged<TT, TO>, blocks, kThreads, kStageSmem, s,
@@ -1412,17 +1451,24 @@ template <class T, int V>
 gs_status small_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, const int32_t* index,
                      float scale, const gs_matrix* dtable, bool accumulate, int32_t* dev_status,
                      cudaStream_t s) {
-  // as many blocks as the table has 4096-element pieces, at most four per SM
+  // a row per block while that leaves at most four blocks for each SM, and
+  // the columns cut where the rows do not fill the device
   const int64_t rows = dtable->rows;
-  int64_t blocks = (rows * dtable->cols + 4095) / 4096;
-  if (blocks > 148 * 4) blocks = 148 * 4;
-  if (blocks > rows) blocks = rows;
-  const int64_t per = (rows + blocks - 1) / blocks;
+  int64_t blocks = rows < 148 * 4 ? rows : 148 * 4;
+  int64_t per = (rows + blocks - 1) / blocks;
+  if (per > kSmallRows) per = kSmallRows;
   blocks = (rows + per - 1) / per;
-  GS_TRY(launch_dependent(k_small_grad<T, V>, (unsigned)blocks, kThreads, 0, s,
-                          static_cast<const T*>(g->data), g->row_stride, g->col_stride, g->cols, ids,
-                          n_ids, index, (int)g->rows, scale, static_cast<float*>(dtable->data),
-                          dtable->row_stride, rows, per, accumulate, dev_status));
+  const int nv = (g->cols + V - 1) / V;
+  int64_t col_tiles = 148 / blocks;
+  if (col_tiles > nv) col_tiles = nv;
+  if (col_tiles < 1) col_tiles = 1;
+  const int share = (int)((nv + col_tiles - 1) / col_tiles);
+  col_tiles = (nv + share - 1) / share;
+  GS_TRY(launch_dependent(k_small_grad<T, V>, (unsigned)(blocks * col_tiles), kThreads, 0, s,
+                          static_cast<const T*>(g->data), g->row_stride, g->col_stride, g->cols,
+                          share, (unsigned)col_tiles, ids, n_ids, index, (int)g->rows, scale,
+                          static_cast<float*>(dtable->data), dtable->row_stride, rows, (int)per,
+                          accumulate, dev_status));
   GS_LAUNCH_CHECK();
   return GS_OK;
 }
