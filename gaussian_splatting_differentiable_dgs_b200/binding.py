@@ -654,7 +654,7 @@ class TensorList:
         self.tensors = list(tensors)
         self.count = len(self.tensors)
         self.array = (gs_tensor * max(self.count, 1))()
-        self.shapes = [t.shape for t in self.tensors]
+        self.shapes = repr([tuple(t.shape) for t in self.tensors])
         self.device = None  # the CUDA device of the tensors, -1 if they are not on one
         for k, t in enumerate(self.tensors):
             code = _codes.get(t.dtype)

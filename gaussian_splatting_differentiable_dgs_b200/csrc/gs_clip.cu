@@ -15,11 +15,11 @@ namespace gs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnitBytes = 32768;  // bytes of a row that a block takes at a time
+constexpr int kUnitShift = 15, kUnitBytes = 1 << kUnitShift;  // of a row, that a block takes at a time
 constexpr int kFlatUnit = 4096;    // elements, where rows are too short for that
 constexpr int kShortRow = 1024;    // columns below which rows are short
 constexpr int kMaxTensors = 256;   // tensors per launch, passed by value
-constexpr int kFewTensors = 16, kSomeTensors = 64;  // ... in tables that are quicker to pass
+constexpr int kFewTensors = 16, kSomeTensors = 64, kManyTensors = 128;  // quicker to pass
 constexpr int kNormBlocks = 148 * 32;
 constexpr int kClipBlocks = 148 * 64;
 
@@ -42,14 +42,14 @@ struct Entry {
   const void* src;
   void* dst;
   int64_t cols, src_stride, dst_stride, size;  // size = rows * cols
-  int64_t unit0;                               // first unit of this tensor
-  int32_t row_units;                           // units per row; 0: rows are short
+  uint32_t unit0;                              // first unit of this tensor
+  uint32_t row_units;                          // units per row; 0: rows are short
   int32_t dtype;
 };
 
 template <int N>
 struct Table {
-  int64_t units;
+  uint32_t units;
   int32_t count;
   Entry t[N];
 };
@@ -273,7 +273,8 @@ bool good_tensor(const gs_tensor& t) {
   if (t.rows == 0 || t.cols == 0) return true;
   if (!t.data || !aligned(t.data, es)) return false;
   if (t.rows > 1 && t.row_stride < t.cols) return false;
-  return t.cols <= INT64_MAX / 8 / t.rows;
+  int64_t bytes;
+  return !__builtin_mul_overflow(t.cols, t.rows, &bytes) && bytes <= INT64_MAX / 8;
 }
 
 bool good_list(const gs_tensor* t, int32_t count) {
@@ -307,16 +308,22 @@ bool pair_up(gs_tensor* a, gs_tensor* b) {
   return a->rows == b->rows && a->cols == b->cols;
 }
 
-// Fills tab with up to N non-empty tensors from *at on; false if one
-// has rows of more units than 32 bits count.
+// Fills tab with up to N non-empty tensors from *at on; false if
+// 32 bits do not count their units.
 template <int N>
 bool fill(Table<N>& tab, const gs_tensor* src, const gs_tensor* dst, int32_t count, int32_t* at) {
   tab.count = 0;
-  tab.units = 0;
+  int64_t units = 0;
   for (; *at < count && tab.count < N; ++*at) {
-    gs_tensor t = src[*at], d = dst ? dst[*at] : t;
+    gs_tensor t = src[*at], d = t;
     if (t.rows == 0 || t.cols == 0) continue;
-    pair_up(&t, &d);
+    if (dst) {
+      d = dst[*at];
+      pair_up(&t, &d);
+    } else if (one_piece(t)) {
+      t.cols *= t.rows;
+      t.rows = 1;
+    }
     Entry& e = tab.t[tab.count++];
     e.src = t.data;
     e.dst = d.data;
@@ -325,13 +332,15 @@ bool fill(Table<N>& tab, const gs_tensor* src, const gs_tensor* dst, int32_t cou
     e.cols = t.cols;
     e.src_stride = t.row_stride;
     e.dst_stride = d.row_stride;
-    e.unit0 = tab.units;
-    const int64_t unit = kUnitBytes / (int64_t)type_size(t.dtype);
-    const int64_t row_units = (t.cols + unit - 1) / unit;
-    if (row_units > INT32_MAX) return false;
-    e.row_units = t.rows > 1 && t.cols < kShortRow ? 0 : (int32_t)row_units;
-    tab.units += e.row_units ? t.rows * row_units : (e.size + kFlatUnit - 1) / kFlatUnit;
+    e.unit0 = (uint32_t)units;
+    const int shift = t.dtype == GS_F32 ? kUnitShift - 2 : kUnitShift - 1;  // elements per unit
+    const int64_t row_units = ((t.cols - 1) >> shift) + 1;
+    const bool is_short = t.rows > 1 && t.cols < kShortRow;
+    e.row_units = is_short ? 0 : (uint32_t)row_units;
+    units += is_short ? (e.size + kFlatUnit - 1) / kFlatUnit : t.rows * row_units;
+    if (units > (int64_t)UINT32_MAX) return false;
   }
+  tab.units = (uint32_t)units;
   return true;
 }
 
@@ -395,6 +404,7 @@ extern "C" gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, doubl
   cudaStream_t s = to_stream(stream);
   if (count <= kFewTensors) return norm_impl<kFewTensors>(tensors, count, part, a, s);
   if (count <= kSomeTensors) return norm_impl<kSomeTensors>(tensors, count, part, a, s);
+  if (count <= kManyTensors) return norm_impl<kManyTensors>(tensors, count, part, a, s);
   return norm_impl<kMaxTensors>(tensors, count, part, a, s);
 }
 
@@ -414,5 +424,6 @@ extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, in
   cudaStream_t s = to_stream(stream);
   if (count <= kFewTensors) return clip_impl<kFewTensors>(src, dst, count, clip, s);
   if (count <= kSomeTensors) return clip_impl<kSomeTensors>(src, dst, count, clip, s);
+  if (count <= kManyTensors) return clip_impl<kManyTensors>(src, dst, count, clip, s);
   return clip_impl<kMaxTensors>(src, dst, count, clip, s);
 }
