@@ -5,6 +5,11 @@
 //   clipped g = c g,   Adam on c g.
 // The norm is a sum over everything before anything can be scaled, so the
 // coefficient stays on the device: Adam (or the clipping copy) reads it.
+// The tensors' descriptors are passed by value, so that a call can be captured
+// into a graph and leaves nothing behind.  Bound by HBM: 59 planes of 6M
+// floats (1.4 GB) take 199 us for the norm (7.1 TB/s) and 405 for the clipped
+// copy (7.0 TB/s read and written).  32 KB units and many short blocks: 16 KB
+// units took 691 us for both against 637, eight blocks per SM 758.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -188,11 +193,12 @@ k_clip_coef(const double* __restrict__ part, int n, const CoefArgs a) {
 }
 
 // Up to kClusterUnits units in one launch: a cluster of 8 blocks, four units
-// at a time each; the blocks' sums meet in the first one's shared memory.
-// Two launches cost 2 us more, and a cluster alone draws too little bandwidth
-// for more than that.
+// in each; the blocks' sums meet in the first one's shared memory.  A launch
+// less is 1.2 us of host time (five small tensors: 12.5 us for norm and clip
+// against 13.8); in a graph one unit takes 2.4 us against 2.8 in two launches,
+// 30 units 3.8 against 2.7.
 constexpr int kCluster = 8, kClusterThreads = 1024;
-constexpr int kClusterUnits = 2 * kCluster * kClusterThreads / kThreads;
+constexpr uint32_t kClusterUnits = kCluster * kClusterThreads / kThreads;
 template <int N>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
 k_norm_cluster(const __grid_constant__ Table<N> tab, const CoefArgs a) {

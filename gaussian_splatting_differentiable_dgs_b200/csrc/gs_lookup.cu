@@ -4,9 +4,11 @@
 // Gaussians, a per-view embedding): out[j] = scale * table[id_j], and
 //   dtable[k] = scale * sum over {j : id_j = k} of g[j].
 // gs_grad_accumulate scatters gradients whose indices are all different;
-// here an index may occur any number of times, so the rows are first sorted
-// by id (the library's stable radix sort) and each run of equal ids is
-// summed in order: no float atomics, the same result on every call.
+// here an index may occur any number of times.  The gradient has three forms,
+// chosen by sizes and layout, none with float atomics, so that equal inputs
+// give equal bits: few items in one launch (k_small_grad), tables that fit in
+// shared memory (k_private_sums), and items sorted by id whose runs are then
+// summed (k_sort_*, k_planes_to_rows, k_run_sums).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -74,7 +76,10 @@ struct Div {
 };
 
 // out in rows: one thread per V columns of an item, kRowIlp items' vectors in
-// flight.  A block takes kThreads * kRowIlp consecutive vectors.
+// flight.  A block takes kThreads * kRowIlp consecutive vectors.  Bound by HBM
+// and by the latency of id and row: 2M x 64 fp32 take 116 us (4.6 TB/s), 2M x
+// 27, whose rows are not aligned to vectors, 102 us (2.3 TB/s); a call of 33 x
+// 32 is 3.2 us on the device.
 constexpr int kRowIlp = 4;
 template <class TT, class TO, int V>
 __global__ void __launch_bounds__(kThreads)
@@ -118,7 +123,8 @@ k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
 // Rows that do not start on 16 bytes are covered by the aligned vectors that
 // they touch and moved into place by selects (by 2 words, by 1, by half a
 // word).  Vectors that reach over the table's first or last byte are read by
-// element.
+// element.  1M x 27 from a bf16 table take 26 us (4.3 TB/s); one load per
+// element and a turn in shared memory took 60.
 template <class TT>
 __device__ __forceinline__ uint4 load_cover(uintptr_t p, uintptr_t first, uintptr_t last) {
   if (p >= first && p + 16 <= last) return __ldg(reinterpret_cast<const uint4*>(p));
@@ -230,9 +236,10 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
 // shared memory by one bulk copy each, and a warp writes four (eight) planes'
 // pieces of 128 items from there, 16 bytes of a row at a time.  The row pitch
 // of 4 words more than a multiple of 16 keeps those reads free of bank
-// conflicts.  Bound by the SMs' requests to L2: 6M x 48 fp32 take 233 us (5.1
-// TB/s written and read); 271 with 16-byte asynchronous copies, 309 with a
-// lane reading its own row (a request for every 32 bytes), 310 with the
+// conflicts.  Bound by the SMs' requests to L2 (76% of the cycles): 6M x 48
+// fp32 take 237 us (5.0 TB/s); 271 with 16-byte asynchronous copies, 309 with
+// a lane reading its own row as above (a request for every 32 bytes; up to 64
+// bytes that is the faster form: 1M x 16 in 33 us against 40), 310 with the
 // planes' pieces turned once more and stored in bulk.
 constexpr int kTurnItems = 256;
 constexpr int kStageVecs = 12, kStagePitch = 4 * kStageVecs + 4;  // words
@@ -278,7 +285,7 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
   const int32_t id = t < items ? id_of(ids, n_ids, index, j0 + t, rows, dev_status) : -1;
   // lanes with the same id share the first one's copy: a row that many items
   // use would otherwise be fetched from one place of L2 by all SMs at once
-  // (64 columns of a one-row table: 584 us without this)
+  // (1M items of a one-row table of 64 columns: 45 us, 584 without this)
   const int leader = __ffs(__match_any_sync(0xffffffffu, id)) - 1;
   const bool fetch = id >= 0 && leader == lane;
   s_from[t] = id >= 0 ? (int16_t)(t - lane + leader) : -1;
@@ -319,9 +326,11 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
 // of each tile of kSortTile items, scans the counts along the tiles, and
 // scatters.  The first pass reads the ids themselves.  An item without a row
 // takes the last id and item -1, which adds nothing, so that the keys need no
-// bit more than the rows do.  Against the library's general 32-bit sort (8
-// bits per pass, an even number of passes, a histogram before them, tiles of
-// 4096) 2.5M items over 2^16 rows take half the time.
+// bit more than the rows do.  Bound by the latency of the ranking in shared
+// memory: 2.5M items over 2^16 rows take 72 us in the six kernels, against 127
+// by the library's general 32-bit sort (8 bits per pass, an even number of
+// passes, a histogram before them, tiles of 4096).  Ranks by ballots over the
+// digit's bits: 20 us a pass, 29 with the match instruction.
 // For few items the kernels' launches are what costs: up to kFewTiles tiles
 // the scatter sums the tiles' counts itself and counts the next pass's digits
 // as it writes (integer atomics: the counts do not depend on their order), so
@@ -557,6 +566,8 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
 // in planes costs a 32-byte sector for every element.  A block copies
 // kTurnItems items of up to 192 bytes' columns into shared memory, a plane's
 // piece at a time, all in flight, and writes the rows as one contiguous piece.
+// Bound by HBM: 2.5M x 48 fp32 take 170 us (5.6 TB/s read and written).  The
+// pieces' length counts: 1 KB here, 181 us with 512 bytes, 207 with 128.
 template <class T>
 struct Turn {
   static constexpr int V = 16 / sizeof(T), kVecs = 12, kCols = kVecs * V;
@@ -628,6 +639,10 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
 // and goes on; a block inside one run writes its sum at 2 block and zeros at
 // 2 block + 1, so that a run's partials are neighbours.  Unused partials have
 // the key kNoRow.  The same kernel sums the partials until one block is left.
+// Bound by HBM at random rows: 2.5M x 48 fp32 take 123 us (3.9 TB/s; a row of
+// 192 bytes costs 256 of DRAM traffic), 130 with the rows in registers, eight
+// in flight; bands of columns small enough to stay in L2 between turning and
+// summing were slower in all (576 us for 24 columns at a time against 498).
 constexpr int kMaxTeams = 128, kRunRowBytes = 40 * 1024, kRunEntries = 1024;
 
 struct RunShape {
@@ -810,7 +825,8 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
 // an item among its warp's equal ids from ballots over the id's bits, as in
 // the sort above), sums the runs of equal ids with teams of threads, each a
 // stretch of the sorted list, joins the teams' partial runs in order, and
-// clears the rows that nothing used.  Every block reads all ids.
+// clears the rows that nothing used.  Every block reads all ids.  Bound by
+// latency: 37 x 16 for 100 rows take 5.3 us on the device.
 constexpr int kSmallItems = 2048, kSmallPer = kSmallItems / kThreads;
 constexpr int kSmallTeams = 64, kSmallRows = 1024;
 
@@ -1015,7 +1031,7 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols, int shar
 // to the table.  The groups are found once for all columns.  g is read once,
 // as it lies; the splits' tables are summed by k_join_tables in order.
 // Bound by instruction issue and the shared memory's latency: 2.5M x 48 for
-// 1024 rows take 262 us against 367 by the sort, 150K x 12 take 23 against
+// 1024 rows take 262 us against 367 by the sort, 150K x 12 take 21 against
 // 44; at 2048 rows, with half the columns per block, it is 441 against 361.
 // For a gradient in rows the sort is faster at any size (300K x 128 for 1000
 // rows: 75 us against 157).
@@ -1149,8 +1165,8 @@ k_private_sums(const T* __restrict__ g, int64_t cs, int all,
     for (int k = t; k < rows; k += threads) o[k] = s_table[((c >> 2) * rows + k) * 4 + (c & 3)];
 }
 
-// dtable[k][c] (+)= scale * sum of partial[split][c][k] over the splits, eight
-// stretches of them at a time.
+// dtable[k][c] (+)= scale * sum of partial[split][c][k] over the splits: eight
+// stretches of them side by side, sixteen loads of each in flight.
 __global__ void __launch_bounds__(kThreads)
 k_join_tables(const float* __restrict__ partial, int64_t splits, int cols, int rows, float scale,
               float* __restrict__ dtable, int64_t ld, bool accumulate) {
