@@ -1063,7 +1063,7 @@ struct PrivShape {
     if (splits < 1) splits = 1;
     per = ((n + splits - 1) / splits + kPrivTile - 1) / kPrivTile * kPrivTile;
     splits = (n + per - 1) / per;
-    partial = (size_t)splits * all * rows * 4;
+    partial = (size_t)splits * ((all + 3) / 4) * rows * 16;
   }
 };
 
@@ -1083,7 +1083,8 @@ k_private_sums(const T* __restrict__ g, int64_t cs, int all,
   const int64_t split = blockIdx.x % splits;
   const int c0 = (int)(blockIdx.x / splits) * cols + 4 * w;  // this warp's first column
   const int64_t first = split * per, last = min(first + per, n);
-  for (int i = t; i < cols * rows; i += threads) s_table[i] = 0.f;
+  for (int i = t; i < cols / 4 * rows; i += threads)
+    reinterpret_cast<float4*>(s_table)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float4* table = reinterpret_cast<float4*>(s_table) + w * rows;
   const uint32_t below = (1u << lane) - 1;
   int buf = 0;
@@ -1159,35 +1160,42 @@ k_private_sums(const T* __restrict__ g, int64_t cs, int all,
     }
   }
   __syncthreads();
-  const int from = (int)(blockIdx.x / splits) * cols, width = min(cols, all - from);
-  float* o = partial + (split * all + from) * rows;
-  for (int c = 0; c < width; ++c, o += rows)
-    for (int k = t; k < rows; k += threads) o[k] = s_table[((c >> 2) * rows + k) * 4 + (c & 3)];
+  // partial[split][four columns][row][4], as the table lies
+  const int quads = (all + 3) / 4, from = (int)(blockIdx.x / splits) * (cols / 4);
+  const int size = min(cols / 4, quads - from) * rows;
+  float4* o = reinterpret_cast<float4*>(partial) + (split * quads + from) * rows;
+  for (int i = t; i < size; i += threads) o[i] = reinterpret_cast<const float4*>(s_table)[i];
 }
 
-// dtable[k][c] (+)= scale * sum of partial[split][c][k] over the splits: eight
-// stretches of them side by side, sixteen loads of each in flight.
+// dtable[k][c] (+)= scale * sum of the splits' tables: a thread sums four
+// columns of a row over one of eight stretches of the splits, sixteen loads in
+// flight, and the stretches are joined in order.
 __global__ void __launch_bounds__(kThreads)
-k_join_tables(const float* __restrict__ partial, int64_t splits, int cols, int rows, float scale,
+k_join_tables(const float4* __restrict__ partial, int64_t splits, int cols, int rows, float scale,
               float* __restrict__ dtable, int64_t ld, bool accumulate) {
   constexpr int PARTS = kThreads / 32;
-  __shared__ float s_sum[PARTS][32];
+  __shared__ float4 s_sum[PARTS][32];
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t total = (int64_t)cols * rows, e = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t total = (int64_t)((cols + 3) / 4) * rows, e = (int64_t)blockIdx.x * 32 + lane;
   const int64_t each = (splits + PARTS - 1) / PARTS, a = w * each, b = min(a + each, splits);
-  float sum = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](const float4& x) { sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w; };
   if (e < total) {
-    const float* p = partial + e;
+    const float4* p = partial + e;
 #pragma unroll 16
-    for (int64_t i = a; i < b; ++i) sum += p[i * total];
+    for (int64_t i = a; i < b; ++i) add(p[i * total]);
   }
   s_sum[w][lane] = sum;
   __syncthreads();
   if (w == 0 && e < total) {
-    for (int k = 1; k < PARTS; ++k) sum += s_sum[k][lane];
-    float* d = dtable + e % rows * ld + e / rows;
-    *d = accumulate ? *d + scale * sum : scale * sum;
+    for (int k = 1; k < PARTS; ++k) add(s_sum[k][lane]);
+    const int c = (int)(e / rows) * 4;
+    float* d = dtable + e % rows * ld + c;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < cols) d[i] = accumulate ? d[i] + scale * v[i] : scale * v[i];
   }
 }
 
@@ -1493,7 +1501,7 @@ template <class T>
 gs_status private_grad(const gs_matrix* g, const Ids& src, float scale, const gs_matrix* dtable,
                        bool accumulate, const PrivShape& ps, float* partial, int32_t* dev_status,
                        cudaStream_t s) {
-  const int64_t join = ((int64_t)g->cols * src.rows + 31) / 32;
+  const int64_t join = (((int64_t)g->cols + 3) / 4 * src.rows + 31) / 32;
   if (join > (int64_t)INT32_MAX || ps.splits * ps.col_groups > (int64_t)INT32_MAX)
     return GS_ERR_UNSUPPORTED;
   static std::atomic<unsigned long long> once{0};
@@ -1503,7 +1511,8 @@ gs_status private_grad(const gs_matrix* g, const Ids& src, float scale, const gs
                           g->rows, ps.per, ps.splits, ps.cols, partial, dev_status));
   GS_LAUNCH_CHECK();
   const int rows = (int)src.rows;
-  GS_TRY(launch_dependent(k_join_tables, (unsigned)join, kThreads, 0, s, partial, ps.splits, g->cols, rows, scale,
+  GS_TRY(launch_dependent(k_join_tables, (unsigned)join, kThreads, 0, s,
+                          reinterpret_cast<const float4*>(partial), ps.splits, g->cols, rows, scale,
                           static_cast<float*>(dtable->data), dtable->row_stride, accumulate));
   GS_LAUNCH_CHECK();
   return GS_OK;
