@@ -643,6 +643,49 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
 // 192 bytes costs 256 of DRAM traffic), 130 with the rows in registers, eight
 // in flight; bands of columns small enough to stay in L2 between turning and
 // summing were slower in all (576 us for 24 columns at a time against 498).
+// d[0 .. V) (+)= scale * sum of the columns that exist; vec: 16-byte stores
+template <int V>
+__device__ __forceinline__ void to_row(float* d, const float* sum, int left, float scale,
+                                       bool accumulate, bool vec) {
+  if (V >= 4 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      if (i >= left) break;
+      float4* p = reinterpret_cast<float4*>(d + i);
+      float4 x = accumulate ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (accumulate) {
+        x.x += scale * sum[i], x.y += scale * sum[i + 1];
+        x.z += scale * sum[i + 2], x.w += scale * sum[i + 3];
+      } else {
+        x = make_float4(scale * sum[i], scale * sum[i + 1], scale * sum[i + 2], scale * sum[i + 3]);
+      }
+      *p = x;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < left) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
+}
+
+// V floats between registers and 16-byte aligned memory (any for V = 1)
+template <int V>
+__device__ __forceinline__ void put_floats(float* d, const float* v) {
+  if (V == 1) *d = *v;
+#pragma unroll
+  for (int i = 0; i + 3 < V; i += 4)
+    *reinterpret_cast<float4*>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int V>
+__device__ __forceinline__ void add_floats(float* v, const float* d) {
+  if (V == 1) *v += *d;
+#pragma unroll
+  for (int i = 0; i + 3 < V; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(d + i);
+    v[i] += x.x, v[i + 1] += x.y, v[i + 2] += x.z, v[i + 3] += x.w;
+  }
+}
+
 constexpr int kMaxTeams = 128, kRunRowBytes = 40 * 1024, kRunEntries = 1024;
 
 struct RunShape {
@@ -669,7 +712,7 @@ template <class T, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
 k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, int64_t n,
            const __grid_constant__ RunShape sh, const T* __restrict__ g, int64_t rs, int cols,
-           float scale, float* __restrict__ dtable, int64_t ld, uint32_t rows, bool accumulate,
+           float scale, float* __restrict__ dtable, int64_t ld, uint32_t rows, bool vec, bool accumulate,
            uint32_t* __restrict__ pkey, float* __restrict__ psum, int ldp, int32_t* dev_status) {
   extern __shared__ __align__(16) unsigned char s_row[];  // [entries][pitch]
   __shared__ bool s_start[kMaxTeams], s_whole[kMaxTeams];
@@ -735,10 +778,7 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   bool head = false, start = false, whole = false;
   float sum[V];
   const auto to_table = [&](uint32_t key) {
-    float* d = dtable + (int64_t)key * ld + c;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (V == 1 || c + i < cols) d[i] = accumulate ? d[i] + scale * sum[i] : scale * sum[i];
+    to_row<V>(dtable + (int64_t)key * ld + c, sum, cols - c, scale, accumulate, vec);
   };
   const auto clear = [&]() {
 #pragma unroll
@@ -747,9 +787,7 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   const auto done = [&](bool tail) {
     if (k == kNoRow) return;
     if (!head && !tail) return to_table(k);
-    float* slot = s_part + (head ? 0 : kThreads * V) + t * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) slot[i] = sum[i];
+    put_floats<V>(s_part + (head ? 0 : kThreads * V) + t * V, sum);
     start = !head;
     whole = head && tail;
   };
@@ -784,20 +822,19 @@ k_run_sums(const uint2* __restrict__ pairs, const uint32_t* __restrict__ keys, i
   const auto leave = [&](int slot, uint32_t key, bool zero) {
     const int64_t p = 2 * blk + slot;
     if (c == 0) pkey[p] = key;
-#pragma unroll
-    for (int i = 0; i < V; ++i) psum[p * ldp + c + i] = zero ? 0.f : sum[i];
+    const float none[V] = {};
+    put_floats<V>(psum + p * ldp + c, zero ? none : sum);
   };
   const auto add_following = [&](int u) {  // -> true if the run leaves the block
     for (; u < used; ++u) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += s_part[(u * width + tv) * V + i];
+      add_floats<V>(sum, s_part + (u * width + tv) * V);
       if (!s_whole[u]) return false;
     }
     return true;
   };
   const auto load = [&](int slot) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = s_part[slot * kThreads * V + t * V + i];
+    clear();
+    add_floats<V>(sum, s_part + slot * kThreads * V + t * V);
   };
   if (team == 0 && before != kNoRow && before == s_key[0]) {
     load(0);
@@ -1310,6 +1347,14 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
   return GS_OK;
 }
 
+// Elements of size es that may move together: a divisor of cols and the
+// stride that keeps every vector of the matrix aligned, at most `most`.
+int vector_of(const void* p, int64_t ld, int cols, int es, int most) {
+  int v = most;
+  while (v > 1 && (cols % v || ld % v || !aligned(p, (size_t)v * es))) v >>= 1;
+  return v;
+}
+
 template <class T, int V, bool FIRST>
 gs_status launch_sums(const uint2* pairs, const uint32_t* keys, int64_t n, const RunShape& sh,
                       const T* g, int64_t rs, int cols, float scale, const gs_matrix* dtable,
@@ -1322,7 +1367,9 @@ gs_status launch_sums(const uint2* pairs, const uint32_t* keys, int64_t n, const
   GS_TRY(launch_dependent(k_run_sums<T, V, FIRST>, (unsigned)(sh.blocks * sh.col_tiles), kThreads,
                           sh.smem, s, pairs, keys, n, sh, g, rs, cols, scale,
                           static_cast<float*>(dtable->data), dtable->row_stride,
-                          (uint32_t)dtable->rows, accumulate, pkey, psum, ldp, dev_status));
+                          (uint32_t)dtable->rows,
+                          vector_of(dtable->data, dtable->row_stride, cols, 4, 4) == 4, accumulate,
+                          pkey, psum, ldp, dev_status));
   GS_LAUNCH_CHECK();
   return GS_OK;
 }
@@ -1341,14 +1388,6 @@ gs_status run_sums(const T* g, int64_t rs, int64_t n, int cols, float scale, con
                                       dev_status, s);
   }
   return st;
-}
-
-// Elements of size es that may move together: a divisor of cols and the
-// stride that keeps every vector of the matrix aligned, at most `most`.
-int vector_of(const void* p, int64_t ld, int cols, int es, int most) {
-  int v = most;
-  while (v > 1 && (cols % v || ld % v || !aligned(p, (size_t)v * es))) v >>= 1;
-  return v;
 }
 
 template <class TT, class TO, int V>
