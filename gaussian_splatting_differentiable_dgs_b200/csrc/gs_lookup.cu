@@ -444,7 +444,7 @@ size_t scatter_smem(int bits) {
 
 // FEW: counts[tile][digit] of this pass; next: those of the next pass (or null)
 template <bool FEW>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 3)
 k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
                const uint32_t* __restrict__ counts, const uint32_t* __restrict__ total,
                uint32_t* __restrict__ next, uint2* __restrict__ out) {
@@ -480,11 +480,15 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
     } else {
       tot[i] = cnt[i] = 0;
       if (in) {
-#pragma unroll 16
-        for (int k = 0; k < (int)gridDim.x; ++k) {
-          const uint32_t c = counts[k * bins + d];
-          tot[i] += c;
-          if (k < (int)blockIdx.x) cnt[i] += c;
+        for (int k0 = 0; k0 < (int)gridDim.x; k0 += 16) {
+          uint32_t c[16];  // all in flight, the last ones too
+#pragma unroll
+          for (int k = 0; k < 16; ++k) c[k] = k0 + k < (int)gridDim.x ? counts[(k0 + k) * bins + d] : 0;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            tot[i] += c[k];
+            if (k0 + k < (int)blockIdx.x) cnt[i] += c[k];
+          }
         }
       }
     }
