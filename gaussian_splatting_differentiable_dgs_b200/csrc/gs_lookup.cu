@@ -1309,6 +1309,8 @@ bool good_matrix(const gs_matrix* m) {
   return m->row_stride == 1 && m->col_stride >= m->rows;
 }
 
+constexpr int kMaxCols = 1 << 30;  // columns are counted in int, rounded up
+
 gs_status check_ids(const int32_t* ids, int64_t n_ids, const int32_t* index, int64_t n) {
   if (n < 0 || n_ids < 0) return GS_ERR_ARG;
   if (n > (int64_t)INT32_MAX) return GS_ERR_UNSUPPORTED;  // positions are int32
@@ -1333,8 +1335,7 @@ gs_status plan_lookup(const int32_t* ids, int64_t n_ids, const int32_t* index, i
     if (p == 0 || !few) {
       GS_TRY(launch_dependent(p == 0 ? k_sort_count<true> : k_sort_count<false>, tiles, kThreads, 0, s,
                               src, from, n, shift, ps.bits, counts, few, few ? ps.count - 1 : 0,
-                              dtable, zeros,
-                              dev_status));
+                              dtable, zeros, dev_status));
       GS_LAUNCH_CHECK();
     }
     uint32_t* next = few && p + 1 < ps.count ? counts + ((size_t)tiles << ps.bits) : nullptr;
@@ -1476,6 +1477,7 @@ extern "C" gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64
                                const int32_t* index, double scale, const gs_matrix* out,
                                int32_t* dev_status, gs_stream stream) {
   if (!good_matrix(table) || !good_matrix(out) || table->cols != out->cols) return GS_ERR_ARG;
+  if (table->cols > kMaxCols) return GS_ERR_UNSUPPORTED;
   const gs_status st = check_ids(ids, n_ids, index, out->rows);
   if (st != GS_OK) return st;
   if (out->rows == 0) return GS_OK;
@@ -1492,7 +1494,9 @@ extern "C" gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64
 
 extern "C" size_t gs_lookup_bwd_workspace_size(int64_t n, int64_t rows, int32_t cols,
                                                int32_t planes) {
-  if (n < 0 || n > (int64_t)INT32_MAX || rows < 1 || rows > (int64_t)INT32_MAX || cols < 1) return 0;
+  if (n < 0 || n > (int64_t)INT32_MAX || rows < 1 || rows > (int64_t)INT32_MAX || cols < 1 ||
+      cols > kMaxCols)
+    return 0;
   const size_t b = carve_lookup(nullptr, 0, n, rows, cols, planes ? 4 : 0).bytes;
   return b > 256 ? b : 256;
 }
@@ -1503,6 +1507,7 @@ extern "C" gs_status gs_lookup_plan(const int32_t* ids, int64_t n_ids, const int
   const gs_status st = check_ids(ids, n_ids, index, n);
   if (st != GS_OK) return st;
   if (rows < 1 || rows > (int64_t)INT32_MAX || cols < 1) return GS_ERR_ARG;
+  if (cols > kMaxCols) return GS_ERR_UNSUPPORTED;
   if (n == 0) return GS_OK;
   const LookupWs w = carve_lookup(ws, ws_bytes, n, rows, cols, 0);
   if (!ws || w.bytes > ws_bytes || ws_bytes < 256) return GS_ERR_CAPACITY;
@@ -1604,7 +1609,8 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
   if (flags & ~(GS_LOOKUP_ACCUMULATE | GS_LOOKUP_PLANNED)) return GS_ERR_ARG;
   if (!good_matrix(g) || !good_matrix(dtable) || g->cols != dtable->cols) return GS_ERR_ARG;
   if (dtable->rows < 1 || dtable->rows > (int64_t)INT32_MAX) return GS_ERR_ARG;
-  if (dtable->dtype != GS_F32 || dtable->col_stride != 1) return GS_ERR_UNSUPPORTED;
+  if (dtable->dtype != GS_F32 || dtable->col_stride != 1 || g->cols > kMaxCols)
+    return GS_ERR_UNSUPPORTED;
   const int64_t n = g->rows, rows = dtable->rows;
   const gs_status st = check_ids(ids, n_ids, index, n);
   if (st != GS_OK) return st;
@@ -1624,8 +1630,11 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
   const int64_t elements = rows * dtable->cols, tiles = (n + kSortTile - 1) / kSortTile;
   const bool fused = plan && !accumulate && dtable->row_stride == dtable->cols &&
                      aligned(dt, 16) && elements <= tiles * 65536;
-  if (!accumulate && !fused && (n == 0 || sorted))
-    GS_TRY(cudaMemset2DAsync(dt, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s));
+  if (!accumulate && !fused && (n == 0 || sorted) &&
+      cudaMemset2DAsync(dt, dtable->row_stride * 4, 0, (size_t)g->cols * 4, rows, s) != cudaSuccess) {
+    (void)cudaGetLastError();  // leave no error for the next call
+    return GS_ERR_CUDA;
+  }
   if (n == 0) return GS_OK;
   if (plan) {
     const gs_status ps = plan_lookup(ids, n_ids, index, n, rows, w, dt, fused ? elements : 0,

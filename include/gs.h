@@ -619,8 +619,8 @@ gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
  * (+= with GS_LOOKUP_ACCUMULATE), fp32, rows contiguous; rows of the table
  * that no item uses get zero.  Items with id_j < 0 or out of range add
  * nothing, whatever their g holds.  The sums are fp32 sums in a fixed order:
- * equal inputs give equal bits.  At most 2^31 - 1
- * items and rows.
+ * equal inputs give equal bits.  At most 2^31 - 1 items and rows and 2^30
+ * columns (gs_lookup: 2^31 - 1 items and 2^30 columns).
  * ws: gs_lookup_bwd_workspace_size(n, rows, cols) bytes, planes: whether g is
  * in planes (col_stride other than 1).  gs_lookup_plan writes the
  * sorted order of ids that stay the same for many gradients into ws;
@@ -652,7 +652,9 @@ typedef struct gs_tensor {
   int32_t reserved;
 } gs_tensor;
 
-/* gs_grad_norm: clip[0] = N = sqrt(sum of the squares of all elements of all
+/* Like every call of sections 10 and 11 these can be captured into a graph,
+ * once a call on the device has loaded the library's code.
+ * gs_grad_norm: clip[0] = N = sqrt(sum of the squares of all elements of all
  * tensors), clip[1] = c = min(1, max_norm / (N + eps)) (device, 8-byte
  * aligned; the sum and both values are formed in fp64 in a fixed order).
  * max_norm and eps must be finite and >= 0.  If N is infinite c = 0, if N is

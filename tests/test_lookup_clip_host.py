@@ -49,6 +49,8 @@ def test_lookup_refusals(b):
     assert call(mat(b, rows=0), good) == A                         # an empty table
     assert call(mat(b, rs=1, cs=4), good) == S                     # a table in planes
     assert call(good, mat(b, rows=2 ** 31), n_ids=2 ** 31) == S
+    wide = mat(b, cols=2 ** 30 + 1, rs=2 ** 31)
+    assert call(wide, wide) == S
     assert call(mat(b, rows=0), mat(b, rows=0)) == b.GS_OK
     assert b.gs_launch_counter() == n0
 
@@ -81,6 +83,9 @@ def test_lookup_gradient_refusals(b):
     assert plan(n=0) == b.GS_OK
     assert L.gs_lookup_bwd_workspace_size(-1, 4, 3, 0) == 0
     assert L.gs_lookup_bwd_workspace_size(4, 0, 3, 0) == 0
+    assert L.gs_lookup_bwd_workspace_size(4, 4, 2 ** 30 + 1, 0) == 0
+    wide = mat(b, cols=2 ** 30 + 1, rs=2 ** 31)
+    assert call(wide, wide) == S and plan(cols=2 ** 30 + 1) == S
     assert 0 < L.gs_lookup_bwd_workspace_size(10, 4, 3, 0) <= L.gs_lookup_bwd_workspace_size(10 ** 6, 4, 3, 1)
     assert b.gs_launch_counter() == n0
 
