@@ -292,7 +292,8 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // Programmatic dependent launch: a kernel launched by launch_dependent may
 // start while the kernel before it on the stream drains; it must call
 // wait_for_prior_grids() in every thread before it touches memory.  Saves
-// about a microsecond per launch in chains of short kernels.
+// about two microseconds per launch in chains of short kernels (the lookup
+// gradient of 262K x 128 bf16, seven launches: 60 us against 73).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void wait_for_prior_grids() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -77,9 +77,11 @@ struct Div {
 
 // out in rows: one thread per V columns of an item, kRowIlp items' vectors in
 // flight.  A block takes kThreads * kRowIlp consecutive vectors.  Bound by HBM
-// and by the latency of id and row: 2M x 64 fp32 take 116 us (4.6 TB/s), 2M x
-// 27, whose rows are not aligned to vectors, 102 us (2.3 TB/s); a call of 33 x
-// 32 is 3.2 us on the device.
+// and by the latency of id and row: 2M x 64 fp32 take 88 us (6.1 TB/s), 2M x
+// 27, whose rows are not aligned to vectors, 102 us (2.3 TB/s; 16 bytes of out
+// per thread, element by element: 111); a call of 33 x 32 is 3.2 us on the
+// device.  16-byte stores of fp32 are marked as streaming (118 us without),
+// the others not: it costs 16-bit outputs 8 to 15%.
 constexpr int kRowIlp = 4;
 template <class TT, class TO, int V>
 __global__ void __launch_bounds__(kThreads)
@@ -110,7 +112,11 @@ k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
       Pack<TO, V> w;
 #pragma unroll
       for (int i = 0; i < V; ++i) w.x[i] = from_f<TO>(has[k] ? scale * to_f(in[k].x[i]) : 0.f);
-      *reinterpret_cast<Pack<TO, V>*>(out + (j0 + at[k]) * rs + c[k]) = w;
+      Pack<TO, V>* to = reinterpret_cast<Pack<TO, V>*>(out + (j0 + at[k]) * rs + c[k]);
+      if constexpr (sizeof(w) == 16 && sizeof(TO) == 4)
+        __stcs(reinterpret_cast<uint4*>(to), *reinterpret_cast<const uint4*>(&w));
+      else
+        *to = w;
     }
   }
 }
@@ -123,8 +129,9 @@ k_lookup_rows(const TT* __restrict__ table, int64_t ld, int64_t rows,
 // Rows that do not start on 16 bytes are covered by the aligned vectors that
 // they touch and moved into place by selects (by 2 words, by 1, by half a
 // word).  Vectors that reach over the table's first or last byte are read by
-// element.  1M x 27 from a bf16 table take 26 us (4.3 TB/s); one load per
-// element and a turn in shared memory took 60.
+// element.  1M x 27 from a bf16 table take 22 us (5.1 TB/s); 26 without the
+// stores marked as streaming, 60 with one load per element and a turn in
+// shared memory.
 template <class TT>
 __device__ __forceinline__ uint4 load_cover(uintptr_t p, uintptr_t first, uintptr_t last) {
   if (p >= first && p + 16 <= last) return __ldg(reinterpret_cast<const uint4*>(p));
@@ -212,7 +219,7 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
   TO* o = out + j;
   uint32_t w[NL];
   const auto store = [&](int c) {
-    *o = from_f<TO>(has ? scale * element<TT>(w, c) : 0.f);
+    __stcs(o, from_f<TO>(has ? scale * element<TT>(w, c) : 0.f));
     o += cs;
     asm volatile("" : "+l"(o));  // one running pointer, not C addresses in registers
   };
