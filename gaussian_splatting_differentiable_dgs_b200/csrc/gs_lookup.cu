@@ -1169,7 +1169,7 @@ k_private_sums(const T* __restrict__ g, int64_t cs, int all,
 #pragma unroll
       for (int k = 0; k < GROUPS; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[k].x[i] = col[i][at(k)];
+        for (int i = 0; i < 4; ++i) x[k].x[i] = __ldcs(col[i] + at(k));
       }
     };
     if (j0 + kPrivTile <= last) fetch_rows([&](int k) { return j0 + lane + k * 32; });
