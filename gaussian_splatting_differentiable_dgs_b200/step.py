@@ -240,9 +240,6 @@ class Stepper:
         # each within the budget)
         if leaf_streams not in (1, 2, 3, 4):
             raise ValueError(f"leaf_streams must be 1 to 4, not {leaf_streams!r}")
-        # l1: the L1 photometric loss; l1_ssim: the composite
-        # (1 - lambda) L1 + lambda (1 - SSIM) of 3DGS training (SkipGS notes,
-        # "loss function / training strategy"), SSIM windows local to each Leaf
         if max_grad_norm is not None and not 0.0 <= float(max_grad_norm) < math.inf:
             raise ValueError(f"max_grad_norm must be finite and not negative, not {max_grad_norm!r}")
         if codebook is not None:
@@ -251,6 +248,9 @@ class Stepper:
         self.codebook = codebook
         self._clip = None     # device {norm, coefficient}
         self._clip_ws = None
+        # l1: the L1 photometric loss; l1_ssim: the composite
+        # (1 - lambda) L1 + lambda (1 - SSIM) of 3DGS training (SkipGS notes,
+        # "loss function / training strategy"), SSIM windows local to each Leaf
         self.loss = loss
         self.ssim_lambda = float(ssim_lambda)
         self.mode = mode
@@ -323,7 +323,8 @@ class Stepper:
         return float(self._last_loss.item())
 
     def last_grad_norm(self) -> float:
-        """The norm of the last update's gradient, before clipping."""
+        """The norm of the last update's gradient, before clipping.  A norm that
+        is not finite scales the gradient by 0 (infinite) or NaN (NaN)."""
         if self._clip is None:
             raise ValueError("no update with max_grad_norm was taken")
         return float(self._clip[0].item())
