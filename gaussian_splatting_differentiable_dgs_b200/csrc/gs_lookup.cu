@@ -579,11 +579,14 @@ k_sort_scatter(const uint2* __restrict__ pairs, int64_t n, int shift, int bits,
 // piece at a time, all in flight, and writes the rows as one contiguous piece.
 // Bound by HBM: 2.5M x 48 fp32 take 170 us (5.6 TB/s read and written).  The
 // pieces' length counts: 1 KB here, 181 us with 512 bytes, 207 with 128.
+// 16-bit planes move two elements at a time: 1.5M x 48 fp16 take 60 us (4.9
+// TB/s), 81 by single elements.
 template <class T>
 struct Turn {
   static constexpr int V = 16 / sizeof(T), kVecs = 12, kCols = kVecs * V;
   static constexpr int kPitch = kTurnItems + 4 / sizeof(T);  // odd in words
   static constexpr size_t kSmem = sizeof(T) * kCols * kPitch;
+  static size_t smem(int vecs) { return vecs < kVecs ? sizeof(T) * vecs * V * kPitch : kSmem; }
 };
 
 template <class T>
@@ -597,13 +600,17 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int64_t j0 = (int64_t)blockIdx.x * kTurnItems;
   const int items = (int)min((int64_t)kTurnItems, n - j0);
+  // whether a 16-bit plane's piece starts half a word in: it lies the same way
+  // in shared memory
+  const unsigned start = (unsigned)((reinterpret_cast<uintptr_t>(g) >> 1) + j0), by = (unsigned)cs;
+  const auto odd = [&](int c) { return sizeof(T) == 2 ? (int)((start + (unsigned)c * by) & 1u) : 0; };
   for (int v0 = 0; v0 < vecs; v0 += kVecs) {
     const int nv = min(kVecs, vecs - v0), c0 = v0 * V;
     for (int c = w; c < nv * V; c += W) {
       const T* p = g + (int64_t)(c0 + c) * cs + j0;
       T* d = s + c * P;
       if (c0 + c >= cols) {
-        for (int j = lane; j < items; j += 32) d[j] = from_f<T>(0.f);
+        for (int j = lane; j < items; j += 32) d[odd(c0 + c) + j] = from_f<T>(0.f);
       } else if (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < kTurnItems / 32; ++k)
@@ -611,10 +618,20 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(d + lane + 32 * k)),
                          "l"(p + lane + 32 * k)
                          : "memory");
-      } else {
+      } else {  // two elements at a time, single ones at the plane piece's ends
+        const int off = odd(c0 + c);
 #pragma unroll
-        for (int k = 0; k < kTurnItems / 32; ++k)
-          if (lane + 32 * k < items) d[lane + 32 * k] = p[lane + 32 * k];
+        for (int k = 0; k < kTurnItems / 64 + 1; ++k) {
+          const int e = 2 * (lane + 32 * k) - off;
+          if (e >= 0 && e + 1 < items) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(d + off + e)),
+                         "l"(p + e)
+                         : "memory");
+          } else {
+            if (e >= 0 && e < items) d[off + e] = p[e];
+            if (e + 1 >= 0 && e + 1 < items) d[off + e + 1] = p[e + 1];
+          }
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -624,7 +641,7 @@ k_planes_to_rows(const T* __restrict__ g, int64_t cs, int cols, int64_t n, uint4
     for (int e = t; e < items * nv; e += kThreads) {
       Pack<T, V> x;
 #pragma unroll
-      for (int i = 0; i < V; ++i) x.x[i] = s[(v * V + i) * P + r];
+      for (int i = 0; i < V; ++i) x.x[i] = s[(v * V + i) * P + odd(c0 + v * V + i) + r];
       *reinterpret_cast<Pack<T, V>*>(out + (j0 + r) * vecs + v0 + v) = x;
       r += dr;
       v += dv;
@@ -1595,7 +1612,8 @@ gs_status lookup_grad(const gs_matrix* g, const int32_t* ids, int64_t n_ids, con
     static std::atomic<unsigned long long> once{0};
     GS_TRY(smem_attrs_once((const void*)k_planes_to_rows<T>, (int)Turn<T>::kSmem, &once));
     GS_TRY(launch_dependent(k_planes_to_rows<T>, (unsigned)((n + kTurnItems - 1) / kTurnItems),
-                            kThreads, Turn<T>::kSmem, s, data, g->col_stride, cols, n, w.rows, vecs));
+                            kThreads, Turn<T>::smem(vecs), s, data, g->col_stride, cols, n, w.rows,
+                            vecs));
     GS_LAUNCH_CHECK();
     return run_sums<T, V>(reinterpret_cast<const T*>(w.rows), (int64_t)vecs * V, n, cols, scale,
                           dtable, accumulate, w, dev_status, s);

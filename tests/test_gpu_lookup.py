@@ -398,3 +398,16 @@ def test_kept_order_with_planes_of_a_small_table(b):
         for x in (planar, g):
             got = b.gs_lookup_bwd(x, ids, torch.empty(rows, cols, device="cuda"), ws, planned=True)
             check_grad(got, exact_grad(g, ids, rows, 1.0))
+
+
+@pytest.mark.parametrize("n", [2049, 3000, 40_001])
+@pytest.mark.parametrize("pad,start", [(0, 0), (1, 0), (2, 1), (5, 3)])
+def test_lookup_gradient_of_16_bit_planes(b, n, pad, start):
+    """Planes of 16-bit types that start and follow at odd places, sorted."""
+    for dtype, cols, rows in ((torch.bfloat16, 12, 5000), (torch.float16, 27, 1100), (torch.float16, 100, 2000)):
+        g = torch.randn(n, cols, generator=gen(n + pad), device="cuda").to(dtype)
+        buf = torch.full((cols * (n + pad) + start,), float("nan"), dtype=dtype, device="cuda")
+        view = buf[start:].view(cols, n + pad)[:, :n].t()
+        view.copy_(g)
+        ids = make_ids(n, rows, n + start)
+        check_grad(run_grad(b, view, ids, rows, scale=0.5), exact_grad(g, ids, rows, 0.5))
