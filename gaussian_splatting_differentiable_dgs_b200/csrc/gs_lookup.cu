@@ -1316,7 +1316,7 @@ LookupWs carve_lookup(void* ws, size_t cap, int64_t n, int64_t rows, int cols, i
   // behind what a kept order needs
   const PrivShape priv(n, rows, cols, planes_es != 0);
   if (priv.use) w.partial = cv.take<float>(priv.partial / 4);
-  else if (planes_es) w.rows = cv.take<uint4>((size_t)n * ((cols * planes_es + 15) / 16));
+  else if (planes_es) w.rows = cv.take<uint4>((size_t)n * (((size_t)cols * planes_es + 15) / 16));
   w.bytes = cv.off;
   return w;
 }
@@ -1439,7 +1439,8 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
                     float scale, const gs_matrix* o, int32_t* dev_status, cudaStream_t s) {
   if (o->col_stride != 1) {
     constexpr int V = 16 / sizeof(TT);
-    const int cols = o->cols, words = (cols * (int)sizeof(TT) + 3) / 4;
+    const int cols = o->cols;
+    const int64_t words = ((int64_t)cols * sizeof(TT) + 3) / 4;
     const int al = vector_of(t->data, t->row_stride, cols, sizeof(TT), 2 * V);
     const unsigned blocks = blocks_for(o->rows);
     if (al >= V && words > 16) {
@@ -1462,9 +1463,7 @@ gs_status lookup_by(const gs_matrix* t, const int32_t* ids, int64_t n_ids, const
       else if (al == V) GS_LOOKUP_PLANES(16, 16);
       else GS_LOOKUP_PLANES(16, 0);
     } else {
-      if (al == 2 * V) GS_LOOKUP_PLANES(48, 32);
-      else if (al == V) GS_LOOKUP_PLANES(48, 16);
-      else GS_LOOKUP_PLANES(48, 0);
+      GS_LOOKUP_PLANES(48, 0);  // aligned rows of that size went above
     }
 #undef GS_LOOKUP_PLANES
     GS_LAUNCH_CHECK();
