@@ -27,7 +27,8 @@ class ColorCodebook:
     the order of the model's SH planes), copied to the device; codes: [n]
     integers in [0, K), or negative for a Gaussian without colour
     coefficients (its SH planes are zero).  Holds Adam's moments of the table
-    and, once a gradient was taken, its workspace."""
+    and its gradient.  Calls on different streams are ordered by the caller,
+    as for any tensor: they share the table and self.grad."""
 
     def __init__(self, table, codes, scale: float = 1.0, device="cuda"):
         self.table = torch.as_tensor(table, dtype=torch.float32).to(device).contiguous().clone()
@@ -43,7 +44,6 @@ class ColorCodebook:
         self.m = torch.zeros_like(self.table)
         self.v = torch.zeros_like(self.table)
         self.grad = torch.zeros_like(self.table)
-        self._ws = None
 
     @property
     def rows(self):
@@ -69,10 +69,25 @@ class ColorCodebook:
 
     def gradient(self, g, cand_idx=None, dev_status=None, stream=None):
         """The table's gradient (self.grad) from the gradient of the SH planes,
-        g: [planes][C] of the candidates cand_idx (or of all Gaussians)."""
+        g: [planes][C] of the candidates cand_idx (or of all Gaussians).  Its
+        workspace (about 4 C (planes + 5) bytes where the table has more than
+        1024 rows) is taken from the caching allocator for the call, on the
+        call's own stream: nothing outlives the call, a later call on another
+        stream cannot be given memory that this one still uses, and the view
+        step counts it in its working set."""
         g = g.t()
         need = B.gs_lookup_bwd_workspace_size(g, self.rows)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need + need // 16, dtype=torch.uint8, device=self.table.device)
-        return B.gs_lookup_bwd(g, self.codes, self.grad, self._ws, scale=self.scale,
+        # in steps of an eighth, so that views of similar size share a block
+        step = 1 << max(need.bit_length() - 4, 8)
+        with torch.cuda.stream(self._on(stream)):
+            ws = torch.empty(-(-need // step) * step, dtype=torch.uint8, device=self.table.device)
+        return B.gs_lookup_bwd(g, self.codes, self.grad, ws, scale=self.scale,
                                index=cand_idx, dev_status=dev_status, stream=stream)
+
+    def _on(self, stream):
+        """`stream` as torch knows streams (a raw handle, 0 among them, too)."""
+        if stream is None or not isinstance(stream, int):
+            return stream
+        if stream == 0:
+            return torch.cuda.default_stream(self.table.device)
+        return torch.cuda.ExternalStream(stream, device=self.table.device)

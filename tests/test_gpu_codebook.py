@@ -187,3 +187,56 @@ def test_codebook_refusals():
             Stepper(model, codebook=cb)
     with pytest.raises(ValueError):
         Stepper(model).last_grad_norm()
+
+
+def test_codebook_gradient_on_another_stream():
+    """Two gradients queued on a side stream, the second with more candidates:
+    memory allocated on the current stream in the meantime belongs to neither."""
+    from gaussian_splatting_differentiable_dgs_b200 import binding as B
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    rng = np.random.default_rng(4)
+    n, K, cols = 400_000, 3000, 12
+    cb = ColorCodebook(np.zeros((K, cols), np.float32), rng.integers(0, K, n), 0.5)
+    g = torch.as_tensor(rng.integers(-8, 9, (cols, n)).astype(np.float32)).cuda()
+    few = g[:, :100_000].contiguous()
+    need = B.gs_lookup_bwd_workspace_size(few.t(), K)
+    want = torch.zeros((K, cols), device="cuda").index_add_(0, cb.codes.long(), g.t()) * 0.5
+    long = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(50):  # keeps the side stream busy while the host goes on
+            long.fill_(1)
+    index = torch.arange(n, dtype=torch.int32, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side, side.cuda_stream):
+        cb.gradient(few, index[:100_000], stream=handle)
+        cb.gradient(g, index, stream=handle)
+    others = [torch.full((need // 8 * k,), 255, dtype=torch.uint8, device="cuda") for k in range(4, 13)]
+    torch.cuda.synchronize()
+    assert all(bool((x == 255).all()) for x in others)
+    assert torch.equal(cb.grad, want)  # sums of small integers are exact
+
+
+def test_codebook_workspace_is_in_the_working_set():
+    """The gradient's workspace counts in peak_ws_bytes of every view, the later
+    ones too: none of it is held between views, where the peak starts from."""
+    from gaussian_splatting_differentiable_dgs_b200 import binding as B
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams = scene(n=60_000, seed=2)
+    rng = np.random.default_rng(1)
+    cb = ColorCodebook(np.zeros((1500, sc.P - 11), np.float32), rng.integers(0, 1500, sc.n))
+    stp = Stepper(GaussianModel(sc.params, sc.n, sc.sh_degree), codebook=cb)
+    target = torch.as_tensor(synth.random_image(160, 120, 1) * 0.5).cuda()
+    for _ in range(3):
+        before = torch.cuda.memory_allocated()
+        stats = stp.run_view(cams[0], target)
+        stp.check()
+        after = torch.cuda.memory_allocated()
+        g = torch.empty((sc.P - 11, stats.n_cand), device="cuda").t()
+        need = B.gs_lookup_bwd_workspace_size(g, 1500)
+        assert stats.n_cand > 10_000 and need > 200 * stats.n_cand
+        assert after - before < 1 << 20
+        assert stats.peak_ws_bytes >= need + 4 * sc.P * stats.n_cand  # beside the compact gradient
+        del g

@@ -185,3 +185,23 @@ def test_codebook_and_stepper_check_their_options():
                {"max_grad_norm": float("inf")}, {"codebook": cb}):
         with pytest.raises(ValueError):
             Stepper(model, device="cpu", **kw)
+
+
+def test_codebook_gradient_keeps_no_workspace(b, monkeypatch):
+    """Each call's workspace ends with the call: one that outlived it could be
+    given up, by a later call that needs more, while its stream still reads it."""
+    import weakref
+    import numpy as np
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    cb = ColorCodebook(np.zeros((1500, 12), np.float32), np.zeros(9000, np.int64), device="cpu")
+    held = []
+
+    def bwd(g, ids, dtable, ws, **kw):
+        assert ws.numel() >= b.gs_lookup_bwd_workspace_size(g, 1500) and dtable is cb.grad
+        held.append(weakref.ref(ws))
+        return dtable
+
+    monkeypatch.setattr(b, "gs_lookup_bwd", bwd)
+    for n in (3000, 9000, 5):
+        cb.gradient(torch.zeros(12, n), cand_idx=torch.zeros(n, dtype=torch.int32))
+    assert [r() for r in held] == [None] * 3
