@@ -375,12 +375,12 @@ k_sort_count(const __grid_constant__ Ids src, uint2* __restrict__ pairs, int64_t
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
       const int64_t j = j0 + i * kThreads;
-      at[i] = j < n ? (src.index ? (int64_t)src.index[j] : j) : -2;
+      at[i] = j < n ? (src.index ? (int64_t)src.index[j] : j) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
       const bool in = at[i] >= 0 && (!src.index || at[i] < src.n_ids);
-      bad |= at[i] != -2 && !in;
+      bad |= j0 + i * kThreads < n && !in;
       id[i] = in ? src.ids[at[i]] : -1;
     }
 #pragma unroll

@@ -411,3 +411,31 @@ def test_lookup_gradient_of_16_bit_planes(b, n, pad, start):
         view.copy_(g)
         ids = make_ids(n, rows, n + start)
         check_grad(run_grad(b, view, ids, rows, scale=0.5), exact_grad(g, ids, rows, 0.5))
+
+
+@pytest.mark.parametrize("n,rows,kind", [(300, 40, "rows"), (9000, 40, "planes"), (9000, 40, "rows"),
+                                         (9000, 3000, "planes"), (200_000, 3000, "rows")])
+def test_gradient_flags_every_index_out_of_range(b, n, rows, kind):
+    """In the one-launch, the private-table and the sorted form and in a plan."""
+    cols, n_ids = 12, 2 * n
+    ids = make_ids(n_ids, rows, 101)
+    index = torch.randint(n_ids, (n,), generator=gen(102), device="cuda", dtype=torch.int32)
+    g = layout(torch.randint(-8, 9, (n, cols), generator=gen(103), device="cuda").float(), kind)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in (None, -1, -2, -3, -2 ** 31, n_ids, 2 ** 31 - 1):
+        at = index.clone()
+        if bad is not None:
+            at[[0, n // 2, n - 1]] = bad
+        ok = at == index
+        got = torch.where(ok, ids[torch.where(ok, at, 0).long()], -1)
+        flag = 0 if bad is None else 2
+        dt = run_grad(b, g, ids, rows, index=at, dev_status=st)
+        assert int(st) == flag, bad
+        st.zero_()
+        # sums of small integers are exact in any order
+        assert torch.equal(dt.double(), exact_grad(g, got, rows, 1.0)[0])
+        if n > 2048:
+            ws = torch.empty(b.gs_lookup_bwd_workspace_size(g, rows), dtype=torch.uint8, device="cuda")
+            b.gs_lookup_plan(ids, n, rows, cols, ws, index=at, dev_status=st)
+            assert int(st) == flag, bad
+            st.zero_()
