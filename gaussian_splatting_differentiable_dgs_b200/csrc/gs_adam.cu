@@ -334,7 +334,7 @@ k_adam_clipped(float* __restrict__ P, float* __restrict__ m, float* __restrict__
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       // a Gaussian without a gradient takes 0, also where c is not finite
-      const float x = col[k] >= 0 ? c * gg[q][k] : 0.0f;
+      const float x = col[k] >= 0 ? clipped(c, gg[q][k]) : 0.0f;
       adam_vals(pp[q][k], mm[q][k], vv[q][k], x, a);
     }
     if (V == 4 && cnt == 4) {

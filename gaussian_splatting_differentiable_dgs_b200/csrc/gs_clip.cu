@@ -238,7 +238,7 @@ k_clip(const __grid_constant__ Table<N> tab, const float* __restrict__ clip) {
     using T = decltype(zero);
     constexpr int V = 16 / sizeof(T);
     if (e.row_units == 0)
-      return short_rows<T>(e, u, [&](const T* p, T* q) { put(q, c * to_f(*p)); });
+      return short_rows<T>(e, u, [&](const T* p, T* q) { put(q, clipped(c, to_f(*p))); });
     const Stretch<T> x(e, u);
     const bool aligned_dst = (reinterpret_cast<uintptr_t>(x.dst + x.head) & 15) == 0;
     Vec<T> buf[kVecs];
@@ -247,14 +247,14 @@ k_clip(const __grid_constant__ Table<N> tab, const float* __restrict__ clip) {
       const int i = threadIdx.x + k * kThreads;
       if (i < x.nv) buf[k].raw = __ldcs(reinterpret_cast<const uint4*>(x.src + x.head) + i);
     }
-    x.ends([&](int i) { put(x.dst + i, c * to_f(x.src[i])); });
+    x.ends([&](int i) { put(x.dst + i, clipped(c, to_f(x.src[i]))); });
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       const int i = threadIdx.x + k * kThreads;
       if (i >= x.nv) break;
       Vec<T> w;
 #pragma unroll
-      for (int j = 0; j < V; ++j) put(&w.x[j], c * to_f(buf[k].x[j]));
+      for (int j = 0; j < V; ++j) put(&w.x[j], clipped(c, to_f(buf[k].x[j])));
       if (aligned_dst) {
         __stcs(reinterpret_cast<uint4*>(x.dst + x.head) + i, w.raw);
       } else {

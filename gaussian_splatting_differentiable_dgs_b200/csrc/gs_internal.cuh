@@ -288,6 +288,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A gradient element clipped by the coefficient c: a coefficient of 0 (an
+// infinite norm) takes infinite elements to 0 like all others, where the
+// product would be NaN; NaN stays NaN.
+__device__ __forceinline__ float clipped(float c, float g) {
+  return c == 0.f && isinf(g) ? 0.f : c * g;
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch: a kernel launched by launch_dependent may
 // start while the kernel before it on the stream drains; it must call

@@ -323,8 +323,9 @@ class Stepper:
         return float(self._last_loss.item())
 
     def last_grad_norm(self) -> float:
-        """The norm of the last update's gradient, before clipping.  A norm that
-        is not finite scales the gradient by 0 (infinite) or NaN (NaN)."""
+        """The norm of the last update's gradient, before clipping.  An infinite
+        norm gives an update of zero gradients (infinite elements count as 0
+        too), a NaN norm one of NaN; check() raises after either."""
         if self._clip is None:
             raise ValueError("no update with max_grad_norm was taken")
         return float(self._clip[0].item())

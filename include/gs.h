@@ -658,13 +658,16 @@ typedef struct gs_tensor {
  * tensors), clip[1] = c = min(1, max_norm / (N + eps)) (device, 8-byte
  * aligned; the sum and both values are formed in fp64 in a fixed order).
  * max_norm and eps must be finite and >= 0.  If N is infinite c = 0, if N is
- * NaN c is NaN, and GS_DEV_NONFINITE is set in both cases.  The tensors'
- * descriptors are read on the host during the call.
+ * NaN c is NaN, and GS_DEV_NONFINITE is set in both cases (clip[0] alone is
+ * infinite, and c and the flag are not, where N itself passes fp32's range).
+ * The tensors' descriptors are read on the host during the call.
  * gs_grad_clip: dst = c * src for every element, rounded once, c = clip[1];
  * src[i] and dst[i] have the same type and as many elements, in the same rows
  * and columns unless one of them is a single piece, and are the same memory
  * (in place) or lie apart (from the first to the last element).
- * gs_adam_clipped: gs_adam on the gradient c * g. */
+ * gs_adam_clipped: gs_adam on the gradient c * g.
+ * In both, c = 0 gives 0 for infinite elements too, so that an infinite norm
+ * leaves no NaN behind; NaN elements stay NaN. */
 size_t gs_grad_norm_workspace_size(int32_t count);
 gs_status gs_grad_norm(const gs_tensor* tensors, int32_t count, double max_norm,
                        double eps, float* clip, void* ws, size_t ws_bytes,

@@ -268,3 +268,44 @@ def test_norm_clip_adam_in_a_graph(b):
         for x, y in zip(got, want + [out, clip]):
             assert torch.equal(x, y)
         check_clip(got[4], [g], 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_an_infinite_element_is_clipped_to_zero(b, dtype):
+    """Norm, clipping copy and Adam end to end: an infinite norm scales every
+    gradient to 0, the infinite ones too; NaN stays NaN."""
+    n, P = 1003, 3
+    for short in (False, True):
+        g = rand((P, n), 11, 1.0, dtype) if not short else rand((n, P + 1), 12, 1.0, dtype)[:, :P]
+        g[1, 2], g[2, 0] = math.inf, -math.inf
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        clip = norm_of(b, [g], 1.0, st=st)
+        assert float(clip[0]) == math.inf and float(clip[1]) == 0.0 and int(st) == 4
+        out = torch.full(g.shape, 3.0, dtype=dtype, device="cuda")
+        b.gs_grad_clip([g], [out], clip)
+        assert (out == 0).all()
+        b.gs_grad_clip([g], [g], clip)
+        assert (g == 0).all()
+    g = rand((P, n), 13, 1.0, dtype)
+    g[1, 2], g[2, 0] = math.inf, math.nan
+    clip = norm_of(b, [g], 1.0)
+    b.gs_grad_clip([g], [g], clip)
+    assert torch.isnan(g).all()
+
+
+@pytest.mark.parametrize("compact", [False, True])
+def test_adam_takes_an_infinite_gradient_as_zero(b, compact):
+    n, P, n_pad = 1003, 5, 1024
+    p, m = rand((P, n_pad), 1), rand((P, n_pad), 2, 1e-2)
+    v = rand((P, n_pad), 3, 1e-2).square()
+    g = rand((P, n), 4)
+    g[0, 0], g[3, 500], g[4, n - 1] = math.inf, -math.inf, math.inf
+    slot = torch.arange(n, dtype=torch.int32, device="cuda").flip(0).contiguous() if compact else None
+    clip = norm_of(b, [g], 1.0)
+    assert float(clip[1]) == 0.0
+    args = b.gs_adam_args(LR, B1, B2, EPS, 7, 0)
+    want = [x.clone() for x in (p, m, v)]
+    b.gs_adam_clipped(p, m, v, g, n, slot, n, n_pad, P, args, clip)
+    b.gs_adam(*want, torch.zeros_like(g), n, slot, n, n_pad, P, args)
+    for x, y in zip((p, m, v), want):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
