@@ -21,6 +21,9 @@ from . import binding as B
 
 SH_PLANE = 11  # first SH plane of the model
 
+INTEGERS = (torch.int8, torch.int16, torch.int32, torch.int64, torch.uint8, torch.uint16,
+            torch.uint32, torch.bool)
+
 
 class ColorCodebook:
     """table: [K][3 (D+1)^2] fp32 rows (coefficient k, channel c at 3 k + c,
@@ -35,11 +38,13 @@ class ColorCodebook:
         if self.table.dim() != 2:
             raise ValueError(f"table must be [K][coefficients], not {tuple(self.table.shape)}")
         codes = torch.as_tensor(codes)
-        if codes.dim() != 1 or codes.is_floating_point():
-            raise ValueError("codes must be a 1-D integer array")
+        if codes.dim() != 1 or codes.dtype not in INTEGERS:
+            raise ValueError("codes must be a 1-D array of integers (of up to 32 bits, or int64)")
+        codes = codes.to(torch.int64)
         if codes.numel() and int(codes.max()) >= self.table.shape[0]:
             raise ValueError(f"code {int(codes.max())} of a table of {self.table.shape[0]} rows")
-        self.codes = codes.to(torch.int32).to(device).contiguous()
+        # every negative code means the same; one below -2^31 would wrap
+        self.codes = codes.clamp(min=-1).to(torch.int32).to(device).contiguous()
         self.scale = float(scale)
         self.m = torch.zeros_like(self.table)
         self.v = torch.zeros_like(self.table)

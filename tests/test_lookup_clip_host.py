@@ -205,3 +205,22 @@ def test_codebook_gradient_keeps_no_workspace(b, monkeypatch):
     for n in (3000, 9000, 5):
         cb.gradient(torch.zeros(12, n), cand_idx=torch.zeros(n, dtype=torch.int32))
     assert [r() for r in held] == [None] * 3
+
+
+def test_codebook_takes_codes_of_every_integer_type():
+    """Negative codes beyond 32 bits mean "no colour" as all negative ones do;
+    they do not wrap to a row."""
+    import numpy as np
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    table = np.zeros((4, 48), np.float32)
+    far = ColorCodebook(table, np.array([-2 ** 32 + 1, -2 ** 31 - 1, -2 ** 31, -2 ** 63, 3, -1]), device="cpu")
+    assert (far.codes < 0).tolist() == [True, True, True, True, False, True] and int(far.codes[4]) == 3
+    for dtype in (np.int8, np.int16, np.int32, np.int64, np.uint8, np.uint16, np.uint32):
+        cb = ColorCodebook(table, np.array([0, 3, 2], dtype), device="cpu")
+        assert cb.codes.tolist() == [0, 3, 2] and cb.codes.dtype == torch.int32
+        with pytest.raises(ValueError):
+            ColorCodebook(table, np.array([0, np.iinfo(dtype).max], dtype), device="cpu")
+    assert ColorCodebook(table, np.array([True, False]), device="cpu").codes.tolist() == [1, 0]
+    for bad in (np.array([1j, 0]), np.array([0.0])):
+        with pytest.raises(ValueError):
+            ColorCodebook(table, bad, device="cpu")
