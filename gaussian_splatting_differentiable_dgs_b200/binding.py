@@ -527,10 +527,11 @@ def _torch_names():
     global _int32, _float32, _get_device, _raw_stream
     import torch
     _codes.update({torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16})
-    _int32, _float32 = torch.int32, torch.float32
     _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _float32 = torch.float32
+    _int32 = torch.int32  # last: its presence tells other threads that all are there
 
 
 def _call(name, dev, stream, fn, *args):

@@ -224,3 +224,26 @@ def test_codebook_takes_codes_of_every_integer_type():
     for bad in (np.array([1j, 0]), np.array([0.0])):
         with pytest.raises(ValueError):
             ColorCodebook(table, bad, device="cpu")
+
+
+def test_first_use_from_two_threads(b, monkeypatch):
+    """A thread that finds the torch names there (_int32 is set) finds all of
+    them, at whatever line another thread is setting them."""
+    import sys
+    for name in ("_int32", "_float32", "_get_device", "_raw_stream"):
+        monkeypatch.setattr(b, name, None)
+    monkeypatch.setattr(b, "_codes", {})
+    seen = []
+
+    def at_line(frame, event, arg):
+        seen.append(b._int32 is None or None not in (b._float32, b._get_device, b._raw_stream)
+                    and len(b._codes) == 3)
+        return at_line
+
+    before = sys.gettrace()
+    sys.settrace(lambda frame, event, arg: at_line if frame.f_code is b._torch_names.__code__ else None)
+    try:
+        b._torch_names()
+    finally:
+        sys.settrace(before)
+    assert len(seen) > 4 and all(seen) and b._int32 is torch.int32
