@@ -706,7 +706,8 @@ def gs_grad_norm(tensors, max_norm, clip, ws, eps=1e-6, dev_status=None, stream=
 
 
 def gs_grad_clip(src, dst, clip, stream=None):
-    """dst[i] = clip[1] * src[i] for lists of tensors (dst may be src)."""
+    """dst[i] = clip[1] * src[i] for lists of tensors (dst may be src).  A tensor
+    that two entries write, or one reads and another writes, is refused."""
     s, d = tensor_list(src), tensor_list(dst)
     if s.shapes != d.shapes:
         raise ValueError(f"tensors of shapes {s.shapes} to clip into {d.shapes}")

@@ -13,6 +13,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <string.h>
+
+#include <memory>
+#include <new>
 
 #include "gs_internal.cuh"
 
@@ -314,6 +318,32 @@ bool pair_up(gs_tensor* a, gs_tensor* b) {
   return a->rows == b->rows && a->cols == b->cols;
 }
 
+// The addresses where a list's tensors start, kept by hashing: finds a tensor
+// that is written twice, or read as one entry and written as another.  Their
+// blocks would race, and a tensor listed twice would be scaled once or twice.
+class Starts {
+ public:
+  // `slots`: a power of two above the number of entries, all 0
+  Starts(uintptr_t* slots, size_t size) : slots_(slots), mask_(size - 1) {}
+  // false if it starts where another entry does, and one of the two is written
+  bool add(const void* p, bool written) {
+    const uintptr_t key = reinterpret_cast<uintptr_t>(p);  // even: two bytes an element at least
+    size_t i = (key * 0x9e3779b97f4a7c15ull) >> 32;        // 2^64 / golden ratio
+    for (;; ++i) {
+      uintptr_t& slot = slots_[i & mask_];
+      if (slot == 0) {
+        slot = key | (uintptr_t)written;
+        return true;
+      }
+      if ((slot & ~(uintptr_t)1) == key && (written || (slot & 1))) return false;
+    }
+  }
+
+ private:
+  uintptr_t* slots_;
+  size_t mask_;
+};
+
 // Fills tab with up to N non-empty tensors from *at on; false if
 // 32 bits do not count their units.
 template <int N>
@@ -418,14 +448,28 @@ extern "C" gs_status gs_grad_clip(const gs_tensor* src, const gs_tensor* dst, in
                                   const float* clip, gs_stream stream) {
   if (!good_list(src, count) || !good_list(dst, count) || !clip || !aligned(clip, 8))
     return GS_ERR_ARG;
+  uintptr_t few[4 * kMaxTensors];
+  std::unique_ptr<uintptr_t[]> many;
+  size_t slots = 4 * kFewTensors;
+  while (slots < 4 * (size_t)count) slots *= 2;
+  if (count > kMaxTensors) {
+    many.reset(new (std::nothrow) uintptr_t[slots]);
+    if (!many) return GS_ERR_CAPACITY;
+  }
+  uintptr_t* table = many ? many.get() : few;
+  memset(table, 0, slots * sizeof(uintptr_t));
+  Starts starts(table, slots);
   for (int32_t i = 0; i < count; ++i) {
     gs_tensor x = src[i], y = dst[i];
     if (!pair_up(&x, &y)) return GS_ERR_ARG;
+    if (extent(x) == 0) continue;
     // in place or apart: a copy that overlaps its source is refused
     const char* a = static_cast<const char*>(x.data);
     const char* b = static_cast<const char*>(y.data);
+    if (!starts.add(b, true)) return GS_ERR_ARG;
     if (a == b && x.row_stride == y.row_stride) continue;
-    if (extent(x) && a < b + extent(y) && b < a + extent(x)) return GS_ERR_ARG;
+    if (a < b + extent(y) && b < a + extent(x)) return GS_ERR_ARG;
+    if (!starts.add(a, false)) return GS_ERR_ARG;
   }
   cudaStream_t s = to_stream(stream);
   if (count <= kFewTensors) return clip_impl<kFewTensors>(src, dst, count, clip, s);

@@ -664,7 +664,10 @@ typedef struct gs_tensor {
  * gs_grad_clip: dst = c * src for every element, rounded once, c = clip[1];
  * src[i] and dst[i] have the same type and as many elements, in the same rows
  * and columns unless one of them is a single piece, and are the same memory
- * (in place) or lie apart (from the first to the last element).
+ * (in place) or lie apart (from the first to the last element).  No element
+ * of dst is another tensor's of either list: a tensor listed twice would be
+ * scaled once or twice.  Two tensors that start together are refused, other
+ * overlaps are not looked for.
  * gs_adam_clipped: gs_adam on the gradient c * g.
  * In both, c = 0 gives 0 for infinite elements too, so that an infinite norm
  * leaves no NaN behind; NaN elements stay NaN. */

@@ -309,3 +309,22 @@ def test_adam_takes_an_infinite_gradient_as_zero(b, compact):
     b.gs_adam(*want, torch.zeros_like(g), n, slot, n, n_pad, P, args)
     for x, y in zip((p, m, v), want):
         assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
+def test_clip_of_neighbours_and_of_a_shared_source(b):
+    """What is not refused: rows between one another's, neighbouring pieces of
+    one buffer in any order, one source for two destinations; more tensors
+    than a launch takes."""
+    buf = torch.arange(1, 7 * 64 + 1, device="cuda", dtype=torch.float32).view(7, 64)
+    keep, clip = buf.clone(), torch.tensor([2.0, 0.5], device="cuda")
+    b.gs_grad_clip([buf[:, 10:40], buf[:, :10], buf[:, 40:64]], [buf[:, 10:40], buf[:, :10], buf[:, 40:64]], clip)
+    assert torch.equal(buf, 0.5 * keep)
+    out = torch.zeros(2, 7, 64, device="cuda")
+    b.gs_grad_clip([buf, buf], [out[1], out[0]], clip)
+    assert torch.equal(out[0], 0.25 * keep) and torch.equal(out[1], 0.25 * keep)
+    flat = torch.arange(1000 * 12, device="cuda", dtype=torch.float32)
+    parts = [flat[12 * k:12 * k + 12] for k in torch.randperm(1000).tolist()]
+    b.gs_grad_clip(parts, parts, clip)
+    assert torch.equal(flat, 0.5 * torch.arange(1000 * 12, device="cuda"))
+    with pytest.raises(b.GsError):
+        b.gs_grad_clip(parts + parts[:1], parts + parts[:1], clip)

@@ -247,3 +247,32 @@ def test_first_use_from_two_threads(b, monkeypatch):
     finally:
         sys.settrace(before)
     assert len(seen) > 4 and all(seen) and b._int32 is torch.int32
+
+
+def test_clip_refuses_a_tensor_twice(b):
+    """A tensor that two entries of the list write, or one reads and another
+    writes, as a parameter that two layers share."""
+    import random
+    L, n0 = b.lib(), b.gs_launch_counter()
+    T = b.gs_tensor
+    piece = lambda at, size: T(at, 1, size, size, 0, 0)
+
+    def clip(src, dst, clip):
+        return L.gs_grad_clip((T * len(src))(*src), (T * len(dst))(*dst), len(src), clip, None)
+
+    a, c, d = piece(4096, 100), piece(8192, 100), piece(16384, 100)
+    rows = T(1 << 20, 4, 10, 30, 0, 0)
+    A, nothing = b.GS_ERR_ARG, piece(4096, 0)
+    assert clip([a, c, a], [a, c, a], 256) == A                    # in place
+    assert clip([a, c], [d, d], 256) == A                          # one destination
+    assert clip([a, c], [c, d], 256) == A                          # read by one, written by the other
+    assert clip([d, c], [c, a], 256) == A
+    assert clip([rows, a, rows], [rows, a, rows], 256) == A
+    assert clip([rows, T(1 << 20, 1, 7, 7, 0, 0)], [rows, T(1 << 20, 1, 7, 7, 0, 0)], 256) == A
+    for size in (17, 256, 257, 3000):
+        many = [piece(1 << 30 | 4096 * k, 1000) for k in range(size)]
+        random.Random(1).shuffle(many)
+        assert clip(many + [many[7]], many + [many[7]], 256) == A
+    # no overlap: only the empty ones get past the checks here, as nothing may launch
+    assert clip([nothing, nothing], [nothing, nothing], 256) == b.GS_OK
+    assert b.gs_launch_counter() == n0
