@@ -602,14 +602,15 @@ typedef struct gs_matrix {
   int32_t dtype;  /* GS_F32, GS_F16 or GS_BF16 */
 } gs_matrix;
 
-/* gs_lookup: out[j][c] = scale * table[id_j][c], rounded once to out's type,
- * for j < out->rows, with id_j = ids[j], or ids[index[j]] if index is not
- * NULL (index: out->rows positions in [0, n_ids); without it n_ids must be at
- * least out->rows).  id_j < 0 gives a row of zeros; an id >= table->rows or an
- * index out of range gives zeros too and sets GS_DEV_BOUNDS.  The table's
- * rows are contiguous (col_stride 1, else GS_ERR_UNSUPPORTED); out has either
- * layout.  Elements of out's buffer outside the matrix stay as they were.
- * out must not overlap the inputs. */
+/* gs_lookup: out[j][c] = scale * table[id_j][c] for j < out->rows: the fp32
+ * product with the scale rounded to fp32, then rounded to out's type (16-bit
+ * values are rounded twice, in the product and in the store).  id_j = ids[j],
+ * or ids[index[j]] if index is not NULL (index: out->rows positions in
+ * [0, n_ids); without it n_ids must be at least out->rows).  id_j < 0 gives a
+ * row of zeros; an id >= table->rows or an index out of range gives zeros too
+ * and sets GS_DEV_BOUNDS.  The table's rows are contiguous (col_stride 1, else
+ * GS_ERR_UNSUPPORTED); out has either layout.  Elements of out's buffer
+ * outside the matrix stay as they were.  out must not overlap the inputs. */
 gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
                     const int32_t* index, double scale, const gs_matrix* out,
                     int32_t* dev_status, gs_stream stream);
@@ -618,8 +619,9 @@ gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
  *   dtable[k][c] = scale * sum over {j : id_j = k} of g[j][c]
  * (+= with GS_LOOKUP_ACCUMULATE), fp32, rows contiguous; rows of the table
  * that no item uses get zero.  Items with id_j < 0 or out of range add
- * nothing, whatever their g holds.  The sums are fp32 sums in a fixed order:
- * equal inputs give equal bits.  At most 2^31 - 1 items and rows and 2^30
+ * nothing, whatever their g holds.  The sums are fp32 sums in a fixed order,
+ * times the scale rounded to fp32: equal inputs give equal bits.  dtable must
+ * not overlap g.  At most 2^31 - 1 items and rows and 2^30
  * columns (gs_lookup: 2^31 - 1 items and 2^30 columns).
  * ws: gs_lookup_bwd_workspace_size(n, rows, cols) bytes, planes: whether g is
  * in planes (col_stride other than 1).  gs_lookup_plan writes the
@@ -661,7 +663,8 @@ typedef struct gs_tensor {
  * NaN c is NaN, and GS_DEV_NONFINITE is set in both cases (clip[0] alone is
  * infinite, and c and the flag are not, where N itself passes fp32's range).
  * The tensors' descriptors are read on the host during the call.
- * gs_grad_clip: dst = c * src for every element, rounded once, c = clip[1];
+ * gs_grad_clip: dst = c * src for every element, c = clip[1]: the fp32 product,
+ * then rounded to the type (16-bit values are rounded twice);
  * src[i] and dst[i] have the same type and as many elements, in the same rows
  * and columns unless one of them is a single piece, and are the same memory
  * (in place) or lie apart (from the first to the last element).  No element

@@ -328,3 +328,12 @@ def test_clip_of_neighbours_and_of_a_shared_source(b):
     assert torch.equal(flat, 0.5 * torch.arange(1000 * 12, device="cuda"))
     with pytest.raises(b.GsError):
         b.gs_grad_clip(parts + parts[:1], parts + parts[:1], clip)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_clip_rounds_the_fp32_product(b, dtype):
+    """The fp32 product, then its rounding to the type: bit for bit."""
+    t, clip = rand(100_003, 21, 1.0, dtype), torch.tensor([3.0, 1 / 3], device="cuda")
+    out = torch.empty_like(t)
+    b.gs_grad_clip([t], [out], clip)
+    assert torch.equal(out, (t.float() * clip[1]).to(dtype))

@@ -439,3 +439,18 @@ def test_gradient_flags_every_index_out_of_range(b, n, rows, kind):
             b.gs_lookup_plan(ids, n, rows, cols, ws, index=at, dev_status=st)
             assert int(st) == flag, bad
             st.zero_()
+
+
+@pytest.mark.parametrize("kind", ["rows", "offset", "planes"])
+def test_lookup_rounds_the_fp32_product(b, kind):
+    """The product of the fp32 scale in fp32, then its rounding to the output's
+    type: bit for bit."""
+    n, rows, scale = 5000, 700, 1 / 3
+    for cols in (12, 27, 48):
+        for tt in (torch.float32, torch.float16, torch.bfloat16):
+            table = torch.randn(rows, cols, generator=gen(111), device="cuda").to(tt)
+            ids = make_ids(n, rows, 112, holes=0.0)
+            for to in (torch.float32, torch.float16, torch.bfloat16):
+                out = b.gs_lookup(table, ids, layout(torch.zeros(n, cols, dtype=to, device="cuda"), kind), scale=scale)
+                product = table.float() * torch.tensor(scale, dtype=torch.float32, device="cuda")
+                assert torch.equal(out, product.to(to)[ids.long()])
