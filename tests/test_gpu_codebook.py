@@ -240,3 +240,51 @@ def test_codebook_workspace_is_in_the_working_set():
         assert after - before < 1 << 20
         assert stats.peak_ws_bytes >= need + 4 * sc.P * stats.n_cand  # beside the compact gradient
         del g
+
+
+def test_codebook_step_of_the_whole_image_mode():
+    """mode="original" takes the same update as the bounded mode."""
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams, params, table, codes = codebook_scene()
+    target = torch.as_tensor(synth.random_image(160, 120, 6) * 0.6).cuda()
+    out = []
+    for mode in ("bounded", "original"):
+        model, cb = GaussianModel(params, sc.n, sc.sh_degree), ColorCodebook(table, codes, 0.75)
+        stp = Stepper(model, budget=200_000, codebook=cb, max_grad_norm=1e-3, mode=mode)
+        stp.run_view(cams[0], target)
+        stp.check()
+        assert not model.m[11:].any()
+        new = cb.table.cpu().numpy()
+        decoded = np.where(codes[:, None] >= 0, np.float32(0.75) * new[np.maximum(codes, 0)], np.float32(0))
+        assert np.array_equal(model.params.cpu().numpy()[11:, :sc.n], decoded.T)
+        out.append((model.m.cpu().numpy()[:11, :sc.n], cb.m.cpu().numpy(), stp.last_grad_norm()))
+    (m0, t0, n0), (m1, t1, n1) = out
+    assert rel_l2(m1, m0) <= 2 * GRAD_TOL and rel_l2(t1, t0) <= 2 * GRAD_TOL
+    assert abs(n1 - n0) <= 2 * GRAD_TOL * n0
+
+
+def test_codebook_gradient_in_a_graph():
+    """Captured with a workspace of the graph's own: eager calls and other
+    allocations between replays do not share it."""
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    rng = np.random.default_rng(5)
+    n, K, cols = 30_000, 3000, 12
+    cb = ColorCodebook(np.zeros((K, cols), np.float32), rng.integers(0, K, 4 * n))
+    codes = cb.codes.long()
+    whole = lambda k: torch.as_tensor(rng.integers(-8, 9, (cols, k)).astype(np.float32)).cuda()
+    exact = lambda g: torch.zeros((K, cols), device="cuda").index_add_(0, codes[:g.shape[1]], g.t())
+    g, more = whole(n), whole(4 * n)
+    cb.gradient(g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cb.gradient(g)
+    for _ in range(3):
+        cb.gradient(more)
+        assert torch.equal(cb.grad, exact(more))
+        others = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(16, 25)]
+        g.copy_(whole(n))
+        graph.replay()
+        assert torch.equal(cb.grad, exact(g))
+        assert all(bool((x == 255).all()) for x in others)

@@ -454,3 +454,154 @@ def test_lookup_rounds_the_fp32_product(b, kind):
                 out = b.gs_lookup(table, ids, layout(torch.zeros(n, cols, dtype=to, device="cuda"), kind), scale=scale)
                 product = table.float() * torch.tensor(scale, dtype=torch.float32, device="cuda")
                 assert torch.equal(out, product.to(to)[ids.long()])
+
+
+# ---- exact sums: whole numbers of at most 8 are exact in every type, and so is
+# ---- every sum of up to 2^21 of them in fp32, in any order
+
+def whole(n, cols, seed, dtype=torch.float32):
+    return torch.randint(-8, 9, (n, cols), generator=gen(seed), device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("n", [33, 2048, 2049, 5000, 40_001, 300_007])
+@pytest.mark.parametrize("cols,kind", [(1, "rows"), (12, "planes"), (27, "padded_planes"), (27, "rows"), (48, "rows"),
+                                       (48, "planes"), (16, "padded"), (64, "offset"), (128, "rows")])
+def test_gradient_of_whole_numbers_is_exact(b, n, cols, kind):
+    """Every form and type, with rows that a large part of the items use: an
+    item dropped, doubled or given to another row changes a sum."""
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        g = whole(n, cols, n, dtype)
+        view = layout(g, kind)
+        for rows, hot, holes in ((1, 0.0, 0.0), (1000, 0.5, 0.02), (1024, 0.0, 0.1), (1025, 0.9, 0.0),
+                                 (3000, 0.3, 0.1), (70_001, 0.0, 0.0), (70_001, 0.6, 0.1)):
+            ids = make_ids(n, rows, n + rows, holes=holes, hot=hot)
+            want = exact_grad(g, ids, rows, 2.0)[0]
+            got = run_grad(b, view, ids, rows, scale=2.0)
+            assert torch.equal(got.double(), want), (dtype, rows, hot)
+            got = run_grad(b, view, ids, rows, scale=-1.0, accumulate=True, dtable=got)
+            assert torch.equal(got.double(), want / 2), (dtype, rows, hot)
+
+
+@pytest.mark.parametrize("n", [700, 20_000, 200_000])  # one launch; up to 64 tiles of the sort; more
+@pytest.mark.parametrize("rows", [900, 1100, 70_001, (1 << 20) + 7])  # one, two, two and three passes
+@pytest.mark.parametrize("kind", ["rows", "planes"])
+def test_kept_order_is_the_one_that_is_summed(b, n, rows, kind):
+    """A plan made through an index; other ids at the gradient's call show
+    whether it goes by the kept order."""
+    cols = 12
+    ids, others = make_ids(2 * n, rows, 121, hot=0.2), make_ids(2 * n, rows, 122)
+    index = torch.randperm(2 * n, generator=gen(123), device="cuda")[:n].to(torch.int32)
+    uses_order = n > 2048 and not (kind == "planes" and rows <= 1024)
+    by = (ids if uses_order else others)[index.long()]
+    ws = torch.empty(b.gs_lookup_bwd_workspace_size(layout(whole(n, cols, 1), kind), rows), dtype=torch.uint8,
+                     device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b.gs_lookup_plan(ids, n, rows, cols, ws, index=index, dev_status=st)
+    dt = torch.full((rows, cols), 3.0, device="cuda")
+    total = torch.zeros((rows, cols), dtype=torch.float64, device="cuda")
+    for k, dtype in enumerate((torch.float32, torch.float16, torch.bfloat16)):
+        g = whole(n, cols, 124 + k, dtype)
+        total += exact_grad(g, by, rows, 1.0)[0]
+        b.gs_lookup_bwd(layout(g, kind), others, dt, ws, index=index, planned=True, accumulate=k > 0, dev_status=st)
+        assert torch.equal(dt.double(), total)
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("n", [20_000, 200_000])
+@pytest.mark.parametrize("kind", ["rows", "planes"])
+def test_sorted_gradient_in_a_graph(b, n, kind):
+    """The sorted form, a plan and a planned gradient, captured and replayed
+    with new ids and gradients."""
+    rows, cols = 3000, 12
+    ids, g = make_ids(n, rows, 131), layout(whole(n, cols, 132), kind)
+    dt, kept = torch.empty(rows, cols, device="cuda"), torch.empty(rows, cols, device="cuda")
+    size = b.gs_lookup_bwd_workspace_size(g, rows)
+    ws, plan = (torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+
+    def calls():
+        b.gs_lookup_bwd(g, ids, dt, ws, scale=2.0)
+        b.gs_lookup_plan(ids, n, rows, cols, plan)
+        b.gs_lookup_bwd(g, ids, kept, plan, planned=True)
+        b.gs_lookup_bwd(g, ids, kept, plan, planned=True, accumulate=True)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for seed in (133, 134, 135):
+        ids.copy_(make_ids(n, rows, seed, hot=0.3))
+        g.copy_(whole(n, cols, seed))
+        ws.fill_(seed)
+        plan.fill_(seed)
+        graph.replay()
+        want = exact_grad(g, ids, rows, 2.0)[0]
+        assert torch.equal(dt.double(), want) and torch.equal(kept.double(), want)
+
+
+@pytest.mark.parametrize("cols", [3, 12, 16, 27, 48, 64, 130])
+def test_lookup_into_planes_through_an_index(b, cols):
+    """Both kernels, aligned and unaligned tables of each type."""
+    n, rows, n_ids = 5001, 300, 9000
+    for k, (tt, to) in enumerate([(torch.float32, torch.float32), (torch.bfloat16, torch.float32),
+                                  (torch.float16, torch.float16)]):
+        for kind in ("rows", "padded", "offset"):
+            table = layout(torch.randn(rows, cols, generator=gen(141 + k), device="cuda").to(tt), kind)
+            ids = make_ids(n_ids, rows, 142)
+            index = torch.randint(n_ids, (n,), generator=gen(143), device="cuda", dtype=torch.int32)
+            buf, out = planes(n, cols, to, pad=5, fill=3.0)
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            b.gs_lookup(table, ids, out, index=index, dev_status=st)
+            got = ids[index.long()]
+            want = torch.where((got >= 0)[:, None], table[got.clamp(min=0).long()].to(to), 0.0)
+            assert torch.equal(out, want) and int(st) == 0 and (buf[:, n:] == 3.0).all()
+            for bad in (-1, -2, n_ids, 2 ** 31 - 1):
+                at = index.clone()
+                at[[0, 77, n - 1]] = bad
+                b.gs_lookup(table, ids, out, index=at, dev_status=st)
+                assert int(st) == 2 and torch.equal(out, torch.where((at == index)[:, None], want, 0.0))
+                st.zero_()
+
+
+def rest_is_zero(dt, used):
+    """No element outside the rows `used` is set."""
+    dt[used] = 0.0
+    return int(torch.count_nonzero(dt)) == 0
+
+
+@pytest.mark.parametrize("n", [300, 2049, 200_000])
+@pytest.mark.parametrize("rows,cols", [(2 ** 20 + 5, 12), (2 ** 26 + 3, 48), (2 ** 31 - 1, 1)])
+def test_large_tables(b, n, rows, cols):
+    """Three and four passes of the sort; table offsets past 2^31 elements."""
+    used = torch.randint(rows, (64,), generator=gen(151), device="cuda", dtype=torch.int32).unique()
+    used = torch.cat([used, torch.tensor([rows - 1, rows - 2, 0], dtype=torch.int32, device="cuda")]).unique()
+    pick = torch.randint(len(used), (n,), generator=gen(152), device="cuda", dtype=torch.int32)
+    pick[::7] = -1
+    ids = torch.where(pick >= 0, used[pick.clamp(min=0).long()], -1)
+    for kind in ("rows", "planes"):
+        g = whole(n, cols, 153)
+        dt = torch.full((rows, cols), 5.0, device="cuda")
+        run_grad(b, layout(g, kind), ids, rows, dtable=dt)
+        assert torch.equal(dt[used.long()].double(), exact_grad(g, pick, len(used), 1.0)[0])
+        assert rest_is_zero(dt, used.long())
+        del dt
+    table = torch.zeros((rows, cols), dtype=torch.float16, device="cuda")
+    table[used.long()] = whole(len(used), cols, 154, torch.float16)
+    for kind in ("rows", "planes"):
+        out = b.gs_lookup(table, ids, layout(torch.ones(n, cols, device="cuda"), kind))
+        assert torch.equal(out, torch.where((ids >= 0)[:, None], table[ids.clamp(min=0).long()].float(), 0.0))
+
+
+def test_planes_turned_past_32_bit_offsets(b):
+    """A gradient in planes of more than 2^31 elements, sorted: turned to rows
+    and summed."""
+    n, cols, rows = 45_000_001, 48, 3000
+    j = torch.arange(n, device="cuda")
+    ids = (j * 7919 % rows).to(torch.int32)
+    g = torch.empty((cols, n), dtype=torch.float16, device="cuda")
+    for c in range(cols):
+        g[c] = (j * (c + 3)) % 17 - 8
+    got = run_grad(b, g.t(), ids, rows)
+    for c in range(cols):
+        want = torch.zeros(rows, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), g[c].double())
+        assert torch.equal(got[:, c].double(), want), c
