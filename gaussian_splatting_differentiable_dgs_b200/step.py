@@ -828,11 +828,19 @@ class Stepper:
                                hooks=hooks)
             stats.append(st)
             loss = self._last_loss if loss is None else loss + self._last_loss
+        base_alloc = torch.cuda.memory_allocated(self.device)
+        torch.cuda.reset_peak_memory_stats(self.device)
         tk = _Timer(timing).tic("project_bwd")
         self._update(self._G, m.n_pad, None, m.n, None)
         _Timer(timing).toc(tk)
+        peak = torch.cuda.max_memory_allocated(self.device) - base_alloc
+        if target is not None and target.is_cuda:
+            peak += target.numel() * target.element_size()
         self._last_loss = loss
-        return _merge_stats(stats)
+        merged = _merge_stats(stats)
+        # a codebook's workspace for the whole model's gradient
+        merged.peak_ws_bytes = max(merged.peak_ws_bytes, int(peak))
+        return merged
 
     def run_view_blocks(self, cam, target, blocks=(8, 8), timing=None, hooks=None):
         """The fixed-block schedule of the BoundedGS page (Figs. 5-6): the

@@ -288,3 +288,30 @@ def test_codebook_gradient_in_a_graph():
         graph.replay()
         assert torch.equal(cb.grad, exact(g))
         assert all(bool((x == 255).all()) for x in others)
+
+
+def test_grouped_update_is_in_the_working_set(monkeypatch):
+    """The grouped schedule's one update sums the codebook's gradient over all
+    Gaussians behind the regions: what it takes counts (here 64 MiB more than
+    its workspace, far above a region's peak)."""
+    from gaussian_splatting_differentiable_dgs_b200 import binding as B
+    from gaussian_splatting_differentiable_dgs_b200.codebook import ColorCodebook
+    from gaussian_splatting_differentiable_dgs_b200.step import GaussianModel, Stepper
+    sc, cams = scene(n=6000, seed=2)
+    rng = np.random.default_rng(1)
+    cb = ColorCodebook(np.zeros((1500, sc.P - 11), np.float32), rng.integers(0, 1500, sc.n))
+    stp = Stepper(GaussianModel(sc.params, sc.n, sc.sh_degree), budget=200_000, codebook=cb)
+    target = torch.as_tensor(synth.random_image(160, 120, 1) * 0.5).cuda()
+    need = B.gs_lookup_bwd_workspace_size(stp.model.params[11:, :sc.n].t(), 1500)
+    gradient = cb.gradient
+
+    def more(*args, **kw):
+        held = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        gradient(*args, **kw)
+        del held
+
+    monkeypatch.setattr(cb, "gradient", more)
+    for _ in range(2):
+        stats = stp.run_view_grouped(cams[0], target, groups=(3, 3))
+        stp.check()
+        assert stats.peak_ws_bytes >= (64 << 20) + need + target.numel() * 4
