@@ -243,11 +243,14 @@ k_lookup_planes(const TT* __restrict__ table, int64_t ld, int64_t rows, int tabl
 // shared memory by one bulk copy each, and a warp writes four (eight) planes'
 // pieces of 128 items from there, 16 bytes of a row at a time.  The row pitch
 // of 4 words more than a multiple of 16 keeps those reads free of bank
-// conflicts.  Bound by the SMs' requests to L2 (76% of the cycles): 6M x 48
-// fp32 take 237 us (5.0 TB/s); 271 with 16-byte asynchronous copies, 309 with
-// a lane reading its own row as above (a request for every 32 bytes; up to 64
-// bytes that is the faster form: 1M x 16 in 33 us against 40), 310 with the
-// planes' pieces turned once more and stored in bulk.
+// conflicts.  6M x 48 fp32 take 218 us (5.5 TB/s); 271 with 16-byte
+// asynchronous copies, 309 with a lane reading its own row as above, 310 with
+// the planes' pieces turned once more and stored in bulk.  A lane's own row
+// costs a request for every 32 bytes; up to 64 bytes that is the faster form
+// (1M x 16: 19 us against 28 by this one, 1M x 12: 18 against 28).  No unit is
+// saturated (1.5M x 48: the SMs' requests to L2 busy 62% of the cycles, DRAM
+// 48%, issue 51%): a block's ids, its rows and its stores wait for one
+// another, and shared memory holds four blocks to an SM.
 constexpr int kTurnItems = 256;
 constexpr int kStageVecs = 12, kStagePitch = 4 * kStageVecs + 4;  // words
 constexpr size_t kStageSmem = sizeof(uint32_t) * kTurnItems * kStagePitch;
@@ -334,8 +337,8 @@ k_lookup_planes_staged(const TT* __restrict__ table, int64_t ld, int64_t rows, i
 // scatters.  The first pass reads the ids themselves.  An item without a row
 // takes the last id and item -1, which adds nothing, so that the keys need no
 // bit more than the rows do.  Bound by the latency of the ranking in shared
-// memory: 2.5M items over 2^16 rows take 72 us in the six kernels, against 127
-// by the library's general 32-bit sort (8 bits per pass, an even number of
+// memory: 2.5M items over 2^16 rows take 59 us in the six kernels; the
+// library's general 32-bit sort took 127 (8 bits per pass, an even number of
 // passes, a histogram before them, tiles of 4096).  Ranks by ballots over the
 // digit's bits: 20 us a pass, 29 with the match instruction.
 // For few items the kernels' launches are what costs: up to kFewTiles tiles
@@ -1096,10 +1099,19 @@ k_small_grad(const T* __restrict__ g, int64_t rs, int64_t cs, int cols, int shar
 // to the table.  The groups are found once for all columns.  g is read once,
 // as it lies; the splits' tables are summed by k_join_tables in order.
 // Bound by instruction issue and the shared memory's latency: 2.5M x 48 for
-// 1024 rows take 262 us against 367 by the sort, 150K x 12 take 21 against
-// 44; at 2048 rows, with half the columns per block, it is 441 against 361.
-// For a gradient in rows the sort is faster at any size (300K x 128 for 1000
-// rows: 75 us against 157).
+// 1024 rows take 241 us against 358 by the sort, 150K x 12 take 21 against 37.
+// Against the number of rows, in us, private tables / sort:
+//   2.5M x     512 rows   1024       1536       2048       4096
+//     3        67/101     67/113     71/113     88/113     124/111
+//    12        70/155     82/168    124/168    124/168     334/167
+//    27       121/239    164/252    240/251    325/251     726/253
+//    48       172/346    241/358    310/358    420/358    1155/359
+// (150K items cross a little later.)  More rows leave a block fewer
+// columns, and g's ids are read again for each.  Up to 1024 rows the form wins
+// by a third or more at every width; up to 2048 by less and at some widths
+// only, and those tables take the sort.  For a gradient in rows the sort is
+// faster at any size (300K x 128 for 1000 rows: 64 us; private tables took
+// 157).
 constexpr int kPrivRows = 1024, kPrivWarps = 8, kPrivTile = 256, kPrivBytes = 96 * 1024;
 
 struct PrivShape {
