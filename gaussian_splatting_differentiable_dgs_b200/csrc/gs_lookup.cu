@@ -11,6 +11,7 @@
 // summed (k_sort_*, k_planes_to_rows, k_run_sums).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <math.h>
 
 #include "gs_internal.cuh"
 
@@ -1643,6 +1644,7 @@ extern "C" gs_status gs_lookup_bwd(const gs_matrix* g, const int32_t* ids, int64
                                    uint32_t flags, void* ws, size_t ws_bytes, int32_t* dev_status,
                                    gs_stream stream) {
   if (flags & ~(GS_LOOKUP_ACCUMULATE | GS_LOOKUP_PLANNED)) return GS_ERR_ARG;
+  if (!isfinite((float)scale)) return GS_ERR_ARG;  // times a sum of 0: NaN in rows that nothing uses
   if (!good_matrix(g) || !good_matrix(dtable) || g->cols != dtable->cols) return GS_ERR_ARG;
   if (dtable->rows < 1 || dtable->rows > (int64_t)INT32_MAX) return GS_ERR_ARG;
   if (dtable->dtype != GS_F32 || dtable->col_stride != 1 || g->cols > kMaxCols)

@@ -620,9 +620,9 @@ gs_status gs_lookup(const gs_matrix* table, const int32_t* ids, int64_t n_ids,
  * (+= with GS_LOOKUP_ACCUMULATE), fp32, rows contiguous; rows of the table
  * that no item uses get zero.  Items with id_j < 0 or out of range add
  * nothing, whatever their g holds.  The sums are fp32 sums in a fixed order,
- * times the scale rounded to fp32: equal inputs give equal bits.  dtable must
- * not overlap g.  At most 2^31 - 1 items and rows and 2^30
- * columns (gs_lookup: 2^31 - 1 items and 2^30 columns).
+ * times the scale rounded to fp32, which must be finite: equal inputs give
+ * equal bits.  dtable must not overlap g.  At most 2^31 - 1 items and rows and
+ * 2^30 columns (gs_lookup: 2^31 - 1 items and 2^30 columns).
  * ws: gs_lookup_bwd_workspace_size(n, rows, cols) bytes, planes: whether g is
  * in planes (col_stride other than 1).  gs_lookup_plan writes the
  * sorted order of ids that stay the same for many gradients into ws;

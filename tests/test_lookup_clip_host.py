@@ -276,3 +276,15 @@ def test_clip_refuses_a_tensor_twice(b):
     # no overlap: only the empty ones get past the checks here, as nothing may launch
     assert clip([nothing, nothing], [nothing, nothing], 256) == b.GS_OK
     assert b.gs_launch_counter() == n0
+
+
+def test_lookup_gradient_refuses_a_scale_that_is_not_finite(b):
+    """Its product with an empty sum would put NaN into rows that no item uses.
+    (A workspace of None is refused next, so that nothing launches.)"""
+    L, n0, m = b.lib(), b.gs_launch_counter(), mat(b)
+    call = lambda scale: L.gs_lookup_bwd(ref(m), 256, 4, None, scale, ref(m), 0, None, 0, None, None)
+    for scale in (float("inf"), -float("inf"), float("nan"), 1e39):
+        assert call(scale) == b.GS_ERR_ARG
+    for scale in (0.0, -3e38, 1e-300):
+        assert call(scale) == b.GS_ERR_CAPACITY
+    assert b.gs_launch_counter() == n0
